@@ -36,6 +36,11 @@ BIMAMBA_FAMILY_SHIFT = 18
 BIMAMBA_CHUNKED_WIDE = 0x2000
 BIMAMBA_M2_NO_CLUSTER = 0x8000
 BIMAMBA_TEST_STARVE = 0x100000
+BIMAMBA_GLR_REVERSE = 0x8
+BIMAMBA_NORM_RMS = 0x10
+BIMAMBA_NORM_GATE_SHARED = 0x20
+BIMAMBA_NORM_GAMMA_SHARED = 0x40
+GLR_CHUNK = 64  # BIMAMBA_GLR_CHUNK
 
 D_STATE = 16
 
@@ -72,6 +77,34 @@ class Params2(ctypes.Structure):
 
 class FwdState2(ctypes.Structure):
     _fields_ = [("S", ctypes.c_void_p), ("conv_xbc", ctypes.c_void_p)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class GlrParams(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("r_bias", ctypes.c_void_p), ("i_bias", ctypes.c_void_p)]
+
+
+class GlrInputs(ctypes.Structure):
+    _fields_ = [("x", Rows), ("r", Rows), ("i", Rows), ("add", Rows), ("z", Rows), ("lengths", ctypes.c_void_p),
+                ("dtype", ctypes.c_int)]
+
+
+class GlrGrads(ctypes.Structure):
+    _fields_ = [("dx", Rows), ("dr", Rows), ("di", Rows), ("dadd", Rows), ("dz", Rows), ("dA", ctypes.c_void_p),
+                ("dr_bias", ctypes.c_void_p), ("di_bias", ctypes.c_void_p), ("dh_in", ctypes.c_void_p)]
+
+
+class BlockNormParams(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("post_w", ctypes.c_void_p), ("gamma", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p), ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("du", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dpost_w", ctypes.c_void_p), ("dgamma", ctypes.c_void_p), ("dbeta", ctypes.c_void_p)]
 
 
 class Inputs2(ctypes.Structure):
@@ -121,6 +154,21 @@ def _load():
     lib.bimamba2_block_step.argtypes = [ctypes.POINTER(FwdState2), ctypes.POINTER(Inputs2), I64, ctypes.POINTER(Params2),
                                         P, I, I, I, I, I, ctypes.POINTER(FwdState2), U, P, SZ, P]
     lib.bimamba2_block_step.restype = I
+    lib.bimamba_glr_workspace_bytes.argtypes = [I, I64, I, I]
+    lib.bimamba_glr_workspace_bytes.restype = SZ
+    lib.bimamba_glr_fwd.argtypes = [ctypes.POINTER(GlrInputs), ctypes.POINTER(GlrParams), P, ctypes.POINTER(Rows),
+                                    P, P, I, I64, I, U, P, SZ, P]
+    lib.bimamba_glr_fwd.restype = I
+    lib.bimamba_glr_bwd.argtypes = [ctypes.POINTER(GlrInputs), ctypes.POINTER(GlrParams), ctypes.POINTER(Rows),
+                                    P, P, ctypes.POINTER(GlrGrads), I, I64, I, U, P, SZ, P]
+    lib.bimamba_glr_bwd.restype = I
+    lib.bimamba_block_norm_fwd.argtypes = [P, P, ctypes.POINTER(BlockNormParams), P, P, P, I, I, I, I64, I, U, P]
+    lib.bimamba_block_norm_fwd.restype = I
+    lib.bimamba_block_norm_workspace_bytes.argtypes = [I, I64, I]
+    lib.bimamba_block_norm_workspace_bytes.restype = SZ
+    lib.bimamba_block_norm_bwd.argtypes = [P, P, P, P, P, ctypes.POINTER(BlockNormParams),
+                                           ctypes.POINTER(BlockNormGrads), I, I, I, I64, I, U, P, SZ, P]
+    lib.bimamba_block_norm_bwd.restype = I
     lib.bimamba_features.argtypes = [ctypes.POINTER(Inputs), ctypes.POINTER(Params), I, I64, I, P, P, P]
     lib.bimamba_features.restype = I
     lib.bimamba_status_string.argtypes = [I]
@@ -510,3 +558,258 @@ def bimamba2_block_step(state, xbc, z, dt, params: dict, out=None, out_dtype=Non
     if rc != BIMAMBA_OK:
         raise BimambaError("bimamba2_block_step", rc)
     return out
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+def _check(t, name: str, shape, dtype, device):
+    """`t` (or None) must have this shape and dtype and lie on `device`."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _rows(t, name: str) -> Rows:
+    """[b, L, D] with contiguous channels (any batch and token strides)."""
+    if t is None:
+        return Rows(None, 0, 0)
+    sb, sl, sd = t.stride()
+    if sd != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name} must have contiguous channels (stride 1 in its last dimension)")
+    return Rows(t.data_ptr(), sb, sl)
+
+
+class _On:
+    """The device of the tensors made current and `stream` made its current
+    stream, so that what is allocated here belongs to the stream that uses
+    it.  `handle` is that stream's."""
+
+    def __init__(self, device, stream):
+        self._ctx = None
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self._ctx = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != device.index:
+                self._ctx = torch.cuda.device(device)
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _workspace_for(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), device=device, dtype=torch.uint8)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def bimamba_glr_workspace_bytes(batch: int, L: int, d_inner: int, backward: bool = False) -> int:
+    return int(lib.bimamba_glr_workspace_bytes(batch, L, d_inner, 1 if backward else 0))
+
+
+def _glr_inputs(x, r, i, params: dict, add, z, lengths):
+    b, L, D = x.shape
+    dev = x.device
+    code = _dtype_code(x.dtype)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    for t, name in ((r, "r"), (i, "i"), (add, "add"), (z, "z")):
+        _check(t, name, x.shape, x.dtype, dev)
+    _check(lengths, "lengths", (b,), torch.int32, dev)
+    for name in ("A", "r_bias", "i_bias"):
+        _check(params.get(name), name, (D,), torch.float32, dev)
+    inp = GlrInputs(_rows(x, "x"), _rows(r, "r"), _rows(i, "i"), _rows(add, "add"), _rows(z, "z"), _ptr(lengths), code)
+    return inp, GlrParams(_ptr(params["A"]), _ptr(params.get("r_bias")), _ptr(params.get("i_bias")))
+
+
+def bimamba_glr_fwd(x, r, i, params: dict, reverse: bool = False, add=None, z=None, lengths=None, h_in=None,
+                    h_out=None, chunk_states=None, out=None, flags: int = 0, workspace=None, stream=None):
+    """Gated linear recurrence over a sequence, one direction.  x, r, i (raw
+    gate activations), add, z: [b, L, D] of one dtype with contiguous channels
+    (column slices of a projection's output will do); params: {"A" [D] <= 0,
+    "r_bias", "i_bias" [D] or absent} fp32; lengths: [b] int32 (padded
+    batches).  h_in, h_out (may be the same): [b, D] fp32 states entering and,
+    written, leaving; chunk_states: [b, ceil(L / GLR_CHUNK), D] fp32, written
+    for bimamba_glr_bwd.  Returns out [b, L, D]."""
+    b, L, D = x.shape
+    dev = x.device
+    inp, par = _glr_inputs(x, r, i, params, add, z, lengths)
+    _check(h_in, "h_in", (b, D), torch.float32, dev)
+    _check(h_out, "h_out", (b, D), torch.float32, dev)
+    _check(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), torch.float32, dev)
+    _check(out, "out", x.shape, x.dtype, dev)
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty(b, L, D, device=dev, dtype=x.dtype)
+        workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D), dev)
+        rc = lib.bimamba_glr_fwd(ctypes.byref(inp), ctypes.byref(par), _ptr(h_in), ctypes.byref(_rows(out, "out")),
+                                 _ptr(h_out), _ptr(chunk_states), b, L, D,
+                                 flags | (BIMAMBA_GLR_REVERSE if reverse else 0), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), on.handle)
+    if rc != BIMAMBA_OK:
+        raise BimambaError("bimamba_glr_fwd", rc)
+    return out
+
+
+def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = False, add=None, z=None, lengths=None,
+                    dh_out=None, dh_in=None, dx=None, dr=None, di=None, flags: int = 0, workspace=None, stream=None):
+    """Gradients of a bimamba_glr_fwd call that was given the same inputs and
+    wrote chunk_states.  dout [b, L, D]: gradient of out; dh_out [b, D] fp32:
+    gradient of h_out; dh_in [b, D] fp32, written (may be dh_out); dx, dr, di:
+    [b, L, D] to write into (column slices of one buffer will do).  Returns
+    {"dx", "dr", "di", "dA", "dr_bias", "di_bias" (where params has them),
+    "dadd" (with add), "dz" (with z)}."""
+    b, L, D = x.shape
+    dev = x.device
+    inp, par = _glr_inputs(x, r, i, params, add, z, lengths)
+    _check(dout, "dout", x.shape, x.dtype, dev)
+    _check(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), torch.float32, dev)
+    _check(dh_out, "dh_out", (b, D), torch.float32, dev)
+    _check(dh_in, "dh_in", (b, D), torch.float32, dev)
+    for t, name in ((dx, "dx"), (dr, "dr"), (di, "di")):
+        _check(t, name, x.shape, x.dtype, dev)
+    with _On(dev, stream) as on:
+        def rows_like(t=None):
+            return t if t is not None else torch.empty(b, L, D, device=dev, dtype=x.dtype)
+
+        res = {"dx": rows_like(dx), "dr": rows_like(dr), "di": rows_like(di)}
+        if add is not None:
+            res["dadd"] = rows_like()
+        if z is not None:
+            res["dz"] = rows_like()
+        for name in ("A", "r_bias", "i_bias"):
+            if params.get(name) is not None:
+                res["d" + name] = torch.empty(D, device=dev, dtype=torch.float32)
+        g = GlrGrads(*(_rows(res.get(k), k) for k in ("dx", "dr", "di", "dadd", "dz")),
+                     *(_ptr(res.get(k)) for k in ("dA", "dr_bias", "di_bias")), _ptr(dh_in))
+        workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D, True), dev)
+        rc = lib.bimamba_glr_bwd(ctypes.byref(inp), ctypes.byref(par), ctypes.byref(_rows(dout, "dout")),
+                                 _ptr(chunk_states), _ptr(dh_out), ctypes.byref(g), b, L, D,
+                                 flags | (BIMAMBA_GLR_REVERSE if reverse else 0), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), on.handle)
+    if rc != BIMAMBA_OK:
+        raise BimambaError("bimamba_glr_bwd", rc)
+    return res
+
+
+# ---------------------------------------------------------------- block norm
+
+def _block_norm_params(b: int, d: int, dev, gate, post_w, gamma, beta, res_scale, eps, rms):
+    flags = BIMAMBA_NORM_RMS if rms else 0
+    if gate is not None:
+        shared = gate.dim() == 1
+        _check(gate, "gate", (d,) if shared else (b, d), torch.float32, dev)
+        flags |= BIMAMBA_NORM_GATE_SHARED if shared else 0
+    _check(post_w, "post_w", (d,), torch.float32, dev)
+    one = gamma if gamma is not None else beta
+    if one is not None:
+        shape = (d,) if one.dim() == 1 else (b, d)
+        _check(gamma, "gamma", shape, torch.float32, dev)
+        _check(beta, "beta", shape, torch.float32, dev)
+        flags |= BIMAMBA_NORM_GAMMA_SHARED if one.dim() == 1 else 0
+    return BlockNormParams(_ptr(gate), _ptr(post_w), _ptr(gamma), _ptr(beta), res_scale, eps), flags
+
+
+def bimamba_block_norm_fwd(x, u=None, gate=None, post_w=None, gamma=None, beta=None, res_scale: float = 1.0,
+                           eps: float = 1e-5, rms: bool = False, dtype=None, norm: bool = True, stats=None,
+                           x_out=None, y=None, stream=None):
+    """Residual sum and norm between two blocks: x_out = res_scale * x + gate *
+    N(u) * post_w (u itself without post_w), y = gamma * N(x_out) + beta.  x
+    [b, L, d] the stream; u [b, L, d] the branch's output, or None (y of the
+    stream alone); gate, gamma, beta fp32 [b, d], or [d] for all rows; post_w [d].
+    dtype: y's without a branch (default x's); norm=False: the sum alone;
+    stats [b, L, 4] fp32, written for bimamba_block_norm_bwd; x_out may be x
+    (in place).  Returns (x_out, y); x_out is x where the stream is unchanged
+    (no branch and res_scale 1), y is None with norm=False."""
+    b, L, d = x.shape
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    ty = u.dtype if u is not None else (dtype or x.dtype)
+    par, flags = _block_norm_params(b, d, dev, gate, post_w, gamma, beta, res_scale, eps, rms)
+    _check(u, "u", x.shape, ty, dev)
+    _check(stats, "stats", (b, L, 4), torch.float32, dev)
+    _check(x_out, "x_out", x.shape, x.dtype, dev)
+    _check(y, "y", x.shape, ty, dev)
+    with _On(dev, stream) as on:
+        stored = x_out
+        if stored is None and (u is not None or res_scale != 1.0):
+            stored = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if y is None and norm:
+            y = torch.empty(b, L, d, device=dev, dtype=ty)
+        rc = lib.bimamba_block_norm_fwd(_ptr(x), _ptr(u), ctypes.byref(par), _ptr(stored), _ptr(y if norm else None),
+                                        _ptr(stats), _dtype_code(x.dtype), _dtype_code(ty), b, L, d, flags, on.handle)
+    if rc != BIMAMBA_OK:
+        raise BimambaError("bimamba_block_norm_fwd", rc)
+    return (x if stored is None else stored), (y if norm else None)
+
+
+def bimamba_block_norm_workspace_bytes(batch: int, L: int, d: int) -> int:
+    return int(lib.bimamba_block_norm_workspace_bytes(batch, L, d))
+
+
+def bimamba_block_norm_bwd(dy, dx_out, x_out, stats, u=None, gate=None, post_w=None, gamma=None,
+                           res_scale: float = 1.0, rms: bool = False, want_dbeta: bool = False,
+                           dbeta_shared: bool | None = None, dx=None, workspace=None, stream=None):
+    """Gradients of bimamba_block_norm_fwd.  dy [b, L, d] (or None: y unused),
+    dx_out [b, L, d] (or None: the stream unused after y); x_out, stats as the
+    forward left them, the rest as it was given.  dx may be dx_out (in place).
+    Returns {"dx", "du" (with u), "dgate", "dpost_w", "dgamma" (where given),
+    "dbeta" (want_dbeta; one [d] with dbeta_shared, by default as gamma)}."""
+    b, L, d = x_out.shape
+    dev = x_out.device
+    if not x_out.is_cuda:
+        raise ValueError("x_out must be a CUDA tensor")
+    if dy is None and dx_out is None:
+        raise ValueError("dy and dx_out are both None")
+    ty = u.dtype if u is not None else (dy.dtype if dy is not None else x_out.dtype)
+    par, flags = _block_norm_params(b, d, dev, gate, post_w, gamma, None, res_scale, 1.0, rms)
+    if gamma is None and dbeta_shared:
+        flags |= BIMAMBA_NORM_GAMMA_SHARED
+    elif gamma is not None and dbeta_shared is not None and dbeta_shared != (gamma.dim() == 1):
+        raise ValueError("dbeta has gamma's layout")
+    _check(dy, "dy", x_out.shape, ty, dev)
+    _check(dx_out, "dx_out", x_out.shape, x_out.dtype, dev)
+    _check(u, "u", x_out.shape, ty, dev)
+    _check(stats, "stats", (b, L, 4), torch.float32, dev)
+    _check(dx, "dx", x_out.shape, x_out.dtype, dev)
+    with _On(dev, stream) as on:
+        def vec(like):
+            return torch.empty(like, device=dev, dtype=torch.float32)
+
+        res = {"dx": dx if dx is not None else torch.empty(b, L, d, device=dev, dtype=x_out.dtype)}
+        if u is not None:
+            res["du"] = torch.empty(b, L, d, device=dev, dtype=ty)
+        if gate is not None:
+            res["dgate"] = vec(gate.shape)
+        if post_w is not None:
+            res["dpost_w"] = vec(post_w.shape)
+        if gamma is not None and dy is not None:
+            res["dgamma"] = vec(gamma.shape)
+        if want_dbeta and dy is not None:
+            res["dbeta"] = vec((d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d))
+        g = BlockNormGrads(*(_ptr(res.get(k)) for k in ("dx", "du", "dgate", "dpost_w", "dgamma", "dbeta")))
+        workspace = _workspace_for(workspace, bimamba_block_norm_workspace_bytes(b, L, d), dev)
+        rc = lib.bimamba_block_norm_bwd(_ptr(dy), _ptr(dx_out), _ptr(x_out), _ptr(u), _ptr(stats), ctypes.byref(par),
+                                        ctypes.byref(g), _dtype_code(x_out.dtype), _dtype_code(ty), b, L, d, flags,
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(), on.handle)
+    if rc != BIMAMBA_OK:
+        raise BimambaError("bimamba_block_norm_bwd", rc)
+    return res

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
@@ -10,14 +11,15 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbimamba.so")
-SOURCES = [os.path.join(CSRC, "bimamba_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("bimamba_api.cu", "glr_api.cu", "block_norm_api.cu")]
+OBJ_DIR = os.path.join(PKG, "_build")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
     [os.path.join(INCLUDE, "bimamba.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-I", INCLUDE, "-I", CSRC,
 ]
 
@@ -34,11 +36,37 @@ def stale() -> bool:
     return any(os.path.getmtime(f) > t for f in DEPS)
 
 
+def _reads(path: str, seen: set) -> set:
+    """The in-tree files that compiling `path` reads (its #include "..." closure)."""
+    if path in seen or not os.path.exists(path):
+        return seen
+    seen.add(path)
+    with open(path) as f:
+        for name in re.findall(r'^\s*#include\s+"([^"]+)"', f.read(), re.M):
+            for folder in (CSRC, INCLUDE):
+                _reads(os.path.join(folder, name), seen)
+    return seen
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """One object per source, the stale ones compiled side by side, then the link."""
     if not force and not stale():
         return LIB
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-o", LIB] + SOURCES
-    subprocess.run(cmd, check=True)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    objs, running = [], []
+    for src in SOURCES:
+        obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        if not force and os.path.exists(obj) and \
+                all(os.path.getmtime(f) <= os.path.getmtime(obj) for f in _reads(src, {os.path.abspath(__file__)})):
+            continue
+        cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-c", "-o", obj, src]
+        running.append((cmd, subprocess.Popen(cmd)))
+    # wait for all of them before reporting the first that failed
+    failed = [(cmd, p.returncode) for cmd, p in running if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+    subprocess.run([nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", LIB] + objs, check=True)
     return LIB
 
 

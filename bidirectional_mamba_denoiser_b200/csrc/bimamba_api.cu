@@ -9,6 +9,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "api_util.h"
 #include "bimamba.h"
 #include "block_fused.cuh"
 #include "carry.cuh"
@@ -38,15 +39,6 @@ constexpr int kWPB = 8;      // warps per CTA (prefix, block step)
 #endif
 constexpr int kPrefixGroup = BIMAMBA_PREFIX_GROUP;
 constexpr int kTBlock = 64;  // longest block of the block step
-constexpr int kMaxBatch = 65535;
-constexpr long long kWaitCycles = 4000000000LL;   // ~2 s at 1.965 GHz
-constexpr long long kStarveWaitCycles = 200000LL;  // ~0.1 ms: the starved test gives up fast
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t elem_size(bimamba_dtype_t t) { return t == BIMAMBA_F32 ? 4 : 2; }
-
-bool dtype_ok(int t) { return t == BIMAMBA_F32 || t == BIMAMBA_BF16; }
 
 // Raise the dynamic shared-memory limit of a kernel once per device.
 int ensure_smem(const void* fn, size_t bytes) {
@@ -61,10 +53,6 @@ int ensure_smem(const void* fn, size_t bytes) {
         return BIMAMBA_ERR_CUDA;
     done.insert({fn, dev});
     return BIMAMBA_OK;
-}
-
-int launch_status() {
-    return cudaGetLastError() == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
 }
 
 // Lanes per channel: the smallest power of two that gives about one resident
@@ -580,13 +568,15 @@ const char* bimamba_status_string(int status) {
 }
 
 int bimamba_device_error(int reset) {
-    unsigned int word = 0;
+    unsigned int word = 0, glr = 0;
     if (cudaMemcpyFromSymbol(&word, bimamba::g_device_error, sizeof(word)) != cudaSuccess) return BIMAMBA_ERR_CUDA;
     if (reset) {
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(bimamba::g_device_error, &zero, sizeof(zero)) != cudaSuccess) return BIMAMBA_ERR_CUDA;
     }
-    return (int)word;
+    // the recurrence's kernels are a module of their own, with their own word
+    if (bimamba::glr_error_word(reset, &glr) != BIMAMBA_OK) return BIMAMBA_ERR_CUDA;
+    return (int)(word | glr);
 }
 
 int bimamba_features(const bimamba_inputs_t* in, const bimamba_params_t* p, int batch, int64_t L, int d_inner,

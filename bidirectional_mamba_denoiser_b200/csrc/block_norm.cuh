@@ -1,0 +1,353 @@
+// block_norm.cuh -- the residual sum and the norms between two blocks,
+// forward and backward ("DiffuMamba: High-Throughput Diffusion LMs with
+// Mamba Backbone", App. A.1 Eq. (10)-(12)).
+//
+// Per token row:  un = N(u) post_w,  x_out = res_scale x + gate un (rounded to
+// the stream's type),  y = gamma N(x_out) + beta.  With n = N(x_out),
+// m = N(u), rs = 1/sigma and means over the row:
+//   dn = gamma dy,  D = dx_out + rs (dn - n mean(dn n) - mean(dn))
+//   dx = res_scale D,  g = gate D,  dgate = sum D un,  dpost_w = sum g m
+//   du = rs_u (g post_w - m mean(g post_w m) - mean(g post_w))   (or g)
+//   dgamma = sum dy n,  dbeta = sum dy
+// (a root-mean-square norm drops the plain means).
+//
+// The work is one read and one write of each row: bound by memory.  A thread
+// owns K groups of V neighbouring columns for every row it visits, so the
+// row stays in registers between its passes (mean, then the centred squares:
+// never a difference of large sums), and the backward's column sums stay in
+// registers over all rows of a block.  Row sums are fp32, through warp
+// shuffles and, for rows wider than a warp, shared memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace bimamba {
+
+constexpr int kBlockNormThreads = 512;  // at most; 128 registers a thread
+
+struct BlockNormParams {
+    const void* x;         // forward: the stream entering; backward: x_out as stored
+    const void* u;         // or null
+    const float* gate;     // or null
+    const float* post_w;   // or null
+    const float* gamma;    // or null
+    const float* beta;     // or null (forward)
+    void* x_out;           // forward, or null
+    void* y;               // forward, or null
+    float* stats;          // [rows][4]; forward: or null
+    const void* dy;        // backward, or null
+    const void* dx_out;    // backward, or null
+    void* dx;
+    void* du;
+    float* part;           // backward: [batch * nseg][4][d] column sums (dgate, dpost_w, dgamma, dbeta), or null
+    float res_scale, eps;
+    int64_t L;
+    int batch, d;
+    int gate_bs, gamma_bs;  // floats between batch rows: d, or 0 when shared
+    int rms;
+    int nseg;               // backward: row segments per batch row
+};
+
+// V neighbouring elements <-> fp32 (V = 8: 16- or 32-byte rows of a 16-byte
+// aligned pointer; V = 1: any).
+template <int V>
+__device__ __forceinline__ void bn_load(const __nv_bfloat16* p, float* v) {
+    if constexpr (V == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+template <int V>
+__device__ __forceinline__ void bn_load(const float* p, float* v) {
+    if constexpr (V == 8) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int V>
+__device__ __forceinline__ void bn_store(__nv_bfloat16* p, const float* v) {
+    if constexpr (V == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        *p = __float2bfloat16_rn(v[0]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void bn_store(float* p, const float* v) {
+    if constexpr (V == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *p = v[0];
+    }
+}
+// The value as the stream's type holds it.
+template <typename T>
+__device__ __forceinline__ float bn_round(float v) {
+    if constexpr (sizeof(T) == 2) return __bfloat162float(__float2bfloat16_rn(v));
+    return v;
+}
+// V entries of an optional fp32 vector, `other` without it.
+template <int V>
+__device__ __forceinline__ void bn_vec(const float* p, int c, float other, float* v) {
+    if (p) {
+        bn_load<V>(p + c, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = other;
+    }
+}
+
+// The sum of v over the row's threads (WARP: the warp; else the block, by
+// the two buffers of `red` in turn, so one barrier a sum is enough).
+template <bool WARP>
+__device__ __forceinline__ float bn_row_sum(float v, float (*red)[32], int& turn) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if constexpr (WARP) return v;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    float* r = red[turn];
+    turn ^= 1;
+    if (lane == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < nw ? r[lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// Mean (0 with rms) and 1/sigma of the row held in v[K][V].
+template <int V, int K, bool WARP>
+__device__ __forceinline__ void bn_stats(const float (&v)[K][V], int col0, int step, int d, int rms, float eps,
+                                         float (*red)[32], int& turn, float& mu, float& rs) {
+    mu = 0.f;
+    if (!rms) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += v[k][e];  // columns past d hold 0
+        mu = bn_row_sum<WARP>(s, red, turn) / (float)d;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (col0 + k * step < d) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) q = fmaf(v[k][e] - mu, v[k][e] - mu, q);
+        }
+    rs = rsqrtf(bn_row_sum<WARP>(q, red, turn) / (float)d + eps);
+}
+
+// One row per block (blockDim.x threads of K groups), or with WARP a row per
+// warp.  V == 8: d % 8 == 0 and every pointer 16-byte aligned.
+template <typename TS, typename TU, int V, int K, bool WARP>
+__global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_kernel(const BlockNormParams p) {
+    __shared__ float red[2][32];
+    int turn = 0;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= p.batch * p.L) return;  // whole warps (WARP) or no block at all
+    const int64_t b = row / p.L;
+    const int d = p.d, lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int col0 = lane * V, step = (WARP ? 32 : blockDim.x) * V;
+    float x[K][V], u[K][V];
+    float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = col0 + k * step;
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[k][e] = u[k][e] = 0.f;
+        if (c < d) {
+            bn_load<V>(static_cast<const TS*>(p.x) + row * d + c, x[k]);
+            if (p.u) bn_load<V>(static_cast<const TU*>(p.u) + row * d + c, u[k]);
+        }
+    }
+    if (p.post_w) bn_stats<V, K, WARP>(u, col0, step, d, p.rms, p.eps, red, turn, st.z, st.w);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = col0 + k * step;
+        if (c >= d) continue;
+        float g[V], w[V];
+        bn_vec<V>(p.gate ? p.gate + b * p.gate_bs : nullptr, c, 1.f, g);
+        if (p.post_w) {
+            bn_vec<V>(p.post_w, c, 1.f, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[k][e] = (u[k][e] - st.z) * st.w * w[e];
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[k][e] = bn_round<TS>(fmaf(g[e], u[k][e], p.res_scale * x[k][e]));
+        if (p.x_out) bn_store<V>(static_cast<TS*>(p.x_out) + row * d + c, x[k]);
+    }
+    if (p.y) {
+        bn_stats<V, K, WARP>(x, col0, step, d, p.rms, p.eps, red, turn, st.x, st.y);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = col0 + k * step;
+            if (c >= d) continue;
+            float g[V], be[V];
+            bn_vec<V>(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, c, 1.f, g);
+            bn_vec<V>(p.beta ? p.beta + b * p.gamma_bs : nullptr, c, 0.f, be);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[k][e] = fmaf(g[e], (x[k][e] - st.x) * st.y, be[e]);
+            bn_store<V>(static_cast<TU*>(p.y) + row * d + c, x[k]);
+        }
+    }
+    if (p.stats && lane == 0) {
+        float* s = p.stats + row * 4;
+        s[0] = st.x, s[1] = st.y, s[2] = st.z, s[3] = st.w;
+    }
+}
+
+// A block (or with WARP each warp) walks the rows of one segment of one batch
+// row and keeps the column sums in registers.
+template <typename TS, typename TU, int V, int K, bool WARP>
+__global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_kernel(const BlockNormParams p) {
+    __shared__ float red[2][32];
+    int turn = 0;
+    const int64_t b = blockIdx.y;
+    const int seg = WARP ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (seg >= p.nseg) return;  // whole warps (WARP) or no block at all
+    const int d = p.d, lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int col0 = lane * V, step = (WARP ? 32 : blockDim.x) * V;
+    float sg[K][V], sw[K][V], sm[K][V], sb[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sg[k][e] = sw[k][e] = sm[k][e] = sb[k][e] = 0.f;
+    const int64_t t0 = p.L * seg / p.nseg, t1 = p.L * (seg + 1) / p.nseg;
+    for (int64_t t = t0; t < t1; ++t) {
+        const int64_t row = b * p.L + t;
+        const float* sp = p.stats + row * 4;
+        const float mu = sp[0], rs = sp[1], mu_u = sp[2], rs_u = sp[3];
+        float n[K][V], dy[K][V], D[K][V], u[K][V];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = col0 + k * step;
+#pragma unroll
+            for (int e = 0; e < V; ++e) n[k][e] = dy[k][e] = D[k][e] = u[k][e] = 0.f;
+            if (c >= d) continue;
+            if (p.dy) {
+                bn_load<V>(static_cast<const TS*>(p.x) + row * d + c, n[k]);
+                bn_load<V>(static_cast<const TU*>(p.dy) + row * d + c, dy[k]);
+            }
+            if (p.dx_out) bn_load<V>(static_cast<const TS*>(p.dx_out) + row * d + c, D[k]);
+            if (p.u) bn_load<V>(static_cast<const TU*>(p.u) + row * d + c, u[k]);
+        }
+        if (p.dy) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                if (c >= d) continue;
+                float ga[V];
+                bn_vec<V>(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, c, 1.f, ga);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    n[k][e] = (n[k][e] - mu) * rs;
+                    sm[k][e] = fmaf(dy[k][e], n[k][e], sm[k][e]);
+                    sb[k][e] += dy[k][e];
+                    dy[k][e] *= ga[e];
+                    s1 += dy[k][e];
+                    s2 = fmaf(dy[k][e], n[k][e], s2);
+                }
+            }
+            s2 = bn_row_sum<WARP>(s2, red, turn) / (float)d;
+            s1 = p.rms ? 0.f : bn_row_sum<WARP>(s1, red, turn) / (float)d;
+        }
+        float t1s = 0.f, t2s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = col0 + k * step;
+            if (c >= d) continue;
+            if (p.dy) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) D[k][e] = fmaf(rs, dy[k][e] - fmaf(n[k][e], s2, s1), D[k][e]);
+            }
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = p.res_scale * D[k][e];
+            bn_store<V>(static_cast<TS*>(p.dx) + row * d + c, o);
+            if (!p.u) continue;
+            float ga[V], w[V];
+            bn_vec<V>(p.gate ? p.gate + b * p.gate_bs : nullptr, c, 1.f, ga);
+            if (p.post_w) {
+                bn_vec<V>(p.post_w, c, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float m = (u[k][e] - mu_u) * rs_u, g = ga[e] * D[k][e], gw = g * w[e];
+                    sg[k][e] = fmaf(D[k][e], m * w[e], sg[k][e]);
+                    sw[k][e] = fmaf(g, m, sw[k][e]);
+                    t1s += gw;
+                    t2s = fmaf(gw, m, t2s);
+                    u[k][e] = m;
+                    D[k][e] = gw;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    sg[k][e] = fmaf(D[k][e], u[k][e], sg[k][e]);
+                    o[e] = ga[e] * D[k][e];
+                }
+                bn_store<V>(static_cast<TU*>(p.du) + row * d + c, o);
+            }
+        }
+        if (p.u && p.post_w) {
+            t2s = bn_row_sum<WARP>(t2s, red, turn) / (float)d;
+            t1s = p.rms ? 0.f : bn_row_sum<WARP>(t1s, red, turn) / (float)d;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                if (c >= d) continue;
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = rs_u * (D[k][e] - fmaf(u[k][e], t2s, t1s));
+                bn_store<V>(static_cast<TU*>(p.du) + row * d + c, o);
+            }
+        }
+    }
+    if (!p.part) return;
+    float* q = p.part + ((int64_t)b * p.nseg + seg) * 4 * d;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = col0 + k * step;
+        if (c >= d) continue;
+        bn_store<V>(q + c, sg[k]);
+        bn_store<V>(q + d + c, sw[k]);
+        bn_store<V>(q + 2 * (int64_t)d + c, sm[k]);
+        bn_store<V>(q + 3 * (int64_t)d + c, sb[k]);
+    }
+}
+
+// The column sums over the partial rows, in row order: of one batch row
+// (blockIdx.z), or of all for the shared vectors.  blockIdx.y: which vector.
+__global__ void block_norm_sums_kernel(const float* part, int nseg, int batch, int d, float* dgate, float* dpost_w,
+                                       float* dgamma, float* dbeta, int gate_shared, int gamma_shared) {
+    const int c = blockIdx.x * blockDim.x + threadIdx.x, which = blockIdx.y;
+    float* out = which == 0 ? dgate : which == 1 ? dpost_w : which == 2 ? dgamma : dbeta;
+    const bool shared = which == 1 || (which == 0 ? gate_shared : gamma_shared);
+    const int64_t b = blockIdx.z;
+    if (c >= d || !out || (shared && b > 0)) return;
+    const int64_t k0 = shared ? 0 : b * nseg, k1 = shared ? (int64_t)batch * nseg : k0 + nseg;
+    float s = 0.f;
+    for (int64_t k = k0; k < k1; ++k) s += part[(k * 4 + which) * d + c];
+    out[(shared ? 0 : b * d) + c] = s;
+}
+
+}  // namespace bimamba

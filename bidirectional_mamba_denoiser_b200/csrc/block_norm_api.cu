@@ -1,0 +1,189 @@
+// block_norm_api.cu -- the C ABI of the block norm (include/bimamba.h):
+// argument checks, launch shapes and dispatch.  The arithmetic is in block_norm.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "api_util.h"
+#include "bimamba.h"
+#include "block_norm.cuh"
+
+namespace {
+
+using bimamba::BlockNormParams;
+using bf16 = __nv_bfloat16;
+
+constexpr int kMaxD = 16384;  // the widest row a block of 512 threads holds, 32 columns each
+
+bool sizes_ok(int batch, int64_t L, int d) {
+    return batch > 0 && batch <= kMaxBatch && L > 0 && d > 0 && L <= 0x7fffffffLL / batch;
+}
+
+int check_common(const bimamba_block_norm_params_t* p, bimamba_dtype_t ts, bimamba_dtype_t tu, int batch, int64_t L,
+                 int d, unsigned flags) {
+    if (!p || !sizes_ok(batch, L, d)) return BIMAMBA_ERR_INVALID_ARG;
+    if (flags & ~(BIMAMBA_NORM_RMS | BIMAMBA_NORM_GATE_SHARED | BIMAMBA_NORM_GAMMA_SHARED))
+        return BIMAMBA_ERR_UNSUPPORTED;
+    if (!dtype_ok(ts) || !dtype_ok(tu) || (ts == BIMAMBA_BF16 && tu == BIMAMBA_F32)) return BIMAMBA_ERR_UNSUPPORTED;
+    if (d > kMaxD) return BIMAMBA_ERR_UNSUPPORTED;
+    if (!aligned(p->gate, 4) || !aligned(p->post_w, 4) || !aligned(p->gamma, 4) || !aligned(p->beta, 4))
+        return BIMAMBA_ERR_MISALIGNED;
+    return BIMAMBA_OK;
+}
+
+void fill_common(BlockNormParams& k, const bimamba_block_norm_params_t* p, int batch, int64_t L, int d,
+                 unsigned flags) {
+    k.gate = p->gate;
+    k.post_w = p->post_w;
+    k.gamma = p->gamma;
+    k.res_scale = p->res_scale;
+    k.L = L;
+    k.batch = batch;
+    k.d = d;
+    k.gate_bs = (flags & BIMAMBA_NORM_GATE_SHARED) ? 0 : d;
+    k.gamma_bs = (flags & BIMAMBA_NORM_GAMMA_SHARED) ? 0 : d;
+    k.rms = (flags & BIMAMBA_NORM_RMS) ? 1 : 0;
+}
+
+// How a row is spread over threads.  8 columns a thread (16-byte accesses)
+// where the width and every pointer allow it, else one; rows of at most
+// 1024 columns to a warp (no barrier), wider ones to a block.
+struct Shape {
+    int vec, k, threads;
+    bool warp;
+};
+
+Shape shape_for(int d, bool vec) {
+    const int groups = vec ? d / 8 : d;
+    if (groups <= 128) return {vec ? 8 : 1, groups <= 32 ? 1 : 4, 256, true};
+    const int most = bimamba::kBlockNormThreads, k = (groups + most - 1) / most;  // vec: up to 4; else up to 32
+    const int per = (groups + k - 1) / k;
+    return {vec ? 8 : 1, vec ? (k == 1 ? 1 : 4) : (k <= 4 ? 4 : 32), (per + 31) / 32 * 32, false};
+}
+
+template <bool BWD, typename TS, typename TU, int V, int K, bool WARP>
+int launch_one(const BlockNormParams& k, const Shape& s, cudaStream_t st) {
+    if constexpr (BWD) {
+        const int per = WARP ? s.threads / 32 : 1;
+        const dim3 grid((unsigned)((k.nseg + per - 1) / per), (unsigned)k.batch);
+        bimamba::block_norm_bwd_kernel<TS, TU, V, K, WARP><<<grid, s.threads, 0, st>>>(k);
+    } else {
+        const int per = WARP ? s.threads / 32 : 1;
+        const unsigned grid = (unsigned)((k.batch * k.L + per - 1) / per);
+        bimamba::block_norm_fwd_kernel<TS, TU, V, K, WARP><<<grid, s.threads, 0, st>>>(k);
+    }
+    return launch_status();
+}
+
+template <bool BWD, typename TS, typename TU>
+int launch_shape(const BlockNormParams& k, const Shape& s, cudaStream_t st) {
+    if (s.warp) {
+        if (s.vec == 8) return s.k == 1 ? launch_one<BWD, TS, TU, 8, 1, true>(k, s, st)
+                                        : launch_one<BWD, TS, TU, 8, 4, true>(k, s, st);
+        return s.k == 1 ? launch_one<BWD, TS, TU, 1, 1, true>(k, s, st)
+                        : launch_one<BWD, TS, TU, 1, 4, true>(k, s, st);
+    }
+    if (s.vec == 8) return s.k == 1 ? launch_one<BWD, TS, TU, 8, 1, false>(k, s, st)
+                                    : launch_one<BWD, TS, TU, 8, 4, false>(k, s, st);
+    return s.k == 4 ? launch_one<BWD, TS, TU, 1, 4, false>(k, s, st)
+                    : launch_one<BWD, TS, TU, 1, 32, false>(k, s, st);
+}
+
+template <bool BWD>
+int launch(const BlockNormParams& k, const Shape& s, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
+    if (ts == BIMAMBA_BF16) return launch_shape<BWD, bf16, bf16>(k, s, st);
+    if (tu == BIMAMBA_BF16) return launch_shape<BWD, float, bf16>(k, s, st);
+    return launch_shape<BWD, float, float>(k, s, st);
+}
+
+// Row segments of the backward per batch row, each with its own column sums:
+// about four blocks an SM in all, and at least 8 rows a segment.
+int segments(int batch, int64_t L) {
+    const int64_t want = std::max<int64_t>(1, 4 * 148 / batch), most = std::max<int64_t>(1, L / 8);
+    return (int)std::min(want, most);
+}
+
+template <typename... P>
+bool all_aligned16(P... p) {
+    return (aligned(p, 16) && ...);
+}
+
+}  // namespace
+
+extern "C" {
+
+int bimamba_block_norm_fwd(const void* x, const void* u, const bimamba_block_norm_params_t* p, void* x_out, void* y,
+                           float* stats, bimamba_dtype_t stream_dtype, bimamba_dtype_t dtype, int batch, int64_t L,
+                           int d, unsigned flags, void* cuda_stream) {
+    int rc = check_common(p, stream_dtype, dtype, batch, L, d, flags);
+    if (rc) return rc;
+    if (!x || (!x_out && !y) || !(p->eps > 0.f)) return BIMAMBA_ERR_INVALID_ARG;
+    if (!u && (p->gate || p->post_w)) return BIMAMBA_ERR_INVALID_ARG;
+    const size_t es = elem_size(stream_dtype), eu = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(x_out, es) || !aligned(u, eu) || !aligned(y, eu) || !aligned(stats, 4))
+        return BIMAMBA_ERR_MISALIGNED;
+
+    BlockNormParams k = {};
+    fill_common(k, p, batch, L, d, flags);
+    k.beta = p->beta;
+    k.eps = p->eps;
+    k.x = x;
+    k.u = u;
+    k.x_out = x_out;
+    k.y = y;
+    k.stats = stats;
+    const bool vec = d % 8 == 0 && all_aligned16(x, u, x_out, y, (const void*)p->gate, (const void*)p->post_w,
+                                                 (const void*)p->gamma, (const void*)p->beta);
+    return launch<false>(k, shape_for(d, vec), stream_dtype, dtype, static_cast<cudaStream_t>(cuda_stream));
+}
+
+size_t bimamba_block_norm_workspace_bytes(int batch, int64_t L, int d) {
+    if (!sizes_ok(batch, L, d)) return 0;
+    return (size_t)batch * segments(batch, L) * 4 * (size_t)d * sizeof(float);
+}
+
+int bimamba_block_norm_bwd(const void* dy, const void* dx_out, const void* x_out, const void* u, const float* stats,
+                           const bimamba_block_norm_params_t* p, const bimamba_block_norm_grads_t* g,
+                           bimamba_dtype_t stream_dtype, bimamba_dtype_t dtype, int batch, int64_t L, int d,
+                           unsigned flags, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+    int rc = check_common(p, stream_dtype, dtype, batch, L, d, flags);
+    if (rc) return rc;
+    if (!g || !x_out || !stats || (!dy && !dx_out) || !g->dx) return BIMAMBA_ERR_INVALID_ARG;
+    if (!u && (p->gate || p->post_w)) return BIMAMBA_ERR_INVALID_ARG;
+    if ((u == nullptr) != (g->du == nullptr)) return BIMAMBA_ERR_INVALID_ARG;
+    if ((g->dgate && !p->gate) || (g->dpost_w && !p->post_w) || (g->dgamma && !p->gamma))
+        return BIMAMBA_ERR_INVALID_ARG;
+    if (!dy && (g->dgamma || g->dbeta)) return BIMAMBA_ERR_INVALID_ARG;
+    const size_t es = elem_size(stream_dtype), eu = elem_size(dtype);
+    if (!aligned(dy, eu) || !aligned(dx_out, es) || !aligned(x_out, es) || !aligned(u, eu) || !aligned(stats, 4) ||
+        !aligned(g->dx, es) || !aligned(g->du, eu) || !aligned(g->dgate, 4) || !aligned(g->dpost_w, 4) ||
+        !aligned(g->dgamma, 4) || !aligned(g->dbeta, 4))
+        return BIMAMBA_ERR_MISALIGNED;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < bimamba_block_norm_workspace_bytes(batch, L, d))
+        return BIMAMBA_ERR_WORKSPACE;
+
+    BlockNormParams k = {};
+    fill_common(k, p, batch, L, d, flags);
+    k.x = x_out;
+    k.u = u;
+    k.stats = const_cast<float*>(stats);
+    k.dy = dy;
+    k.dx_out = dx_out;
+    k.dx = g->dx;
+    k.du = g->du;
+    k.nseg = segments(batch, L);
+    const bool sums = g->dgate || g->dpost_w || g->dgamma || g->dbeta;
+    k.part = sums ? static_cast<float*>(workspace) : nullptr;
+    const bool vec = d % 8 == 0 && all_aligned16(dy, dx_out, x_out, u, (const void*)g->dx, (const void*)g->du,
+                                                 (const void*)p->gate, (const void*)p->post_w, (const void*)p->gamma);
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if ((rc = launch<true>(k, shape_for(d, vec), stream_dtype, dtype, st)) || !sums) return rc;
+    const dim3 grid((unsigned)((d + 127) / 128), 4, (unsigned)batch);
+    bimamba::block_norm_sums_kernel<<<grid, 128, 0, st>>>(
+        k.part, k.nseg, batch, d, g->dgate, g->dpost_w, g->dgamma, g->dbeta, (flags & BIMAMBA_NORM_GATE_SHARED) != 0,
+        (flags & BIMAMBA_NORM_GAMMA_SHARED) != 0);
+    return launch_status();
+}
+
+}  // extern "C"

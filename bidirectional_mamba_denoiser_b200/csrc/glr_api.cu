@@ -1,0 +1,172 @@
+// glr_api.cu -- the C ABI of the gated linear recurrence (include/bimamba.h):
+// argument checks, launch shapes and dispatch.  The arithmetic is in glr.cuh.
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "bimamba.h"
+#include "glr.cuh"
+
+namespace {
+
+using bimamba::GlrParams;
+using bimamba::GlrRows;
+using bf16 = __nv_bfloat16;
+
+static_assert(bimamba::kGlrChunk == BIMAMBA_GLR_CHUNK, "the header's chunk is the kernels'");
+
+bool sizes_ok(int batch, int64_t L, int D) {
+    return batch > 0 && batch <= kMaxBatch && L > 0 && L <= 0x7fffffffLL && D > 0;
+}
+
+// Rows that are read: any strides from 0.
+int check_in(const bimamba_rows_t& q, size_t esz, bool optional) {
+    if (!q.ptr) return optional ? BIMAMBA_OK : BIMAMBA_ERR_INVALID_ARG;
+    if (q.batch_stride < 0 || q.token_stride < 0) return BIMAMBA_ERR_INVALID_ARG;
+    return aligned(q.ptr, esz) ? BIMAMBA_OK : BIMAMBA_ERR_MISALIGNED;
+}
+
+// Rows that are written: no two of them may overlap, so the strides have to
+// nest one way or the other ([batch][L] or [L][batch] order).
+int check_out(const bimamba_rows_t& q, size_t esz, int batch, int64_t L, int D) {
+    int rc = check_in(q, esz, false);
+    if (rc) return rc;
+    const bool tok = L == 1 || q.token_stride >= D, bat = batch == 1 || q.batch_stride >= D;
+    if (!tok || !bat) return BIMAMBA_ERR_INVALID_ARG;
+    if (batch > 1 && L > 1) {
+        const bool batch_outer = (q.batch_stride - D) / q.token_stride >= L - 1;
+        const bool token_outer = (q.token_stride - D) / q.batch_stride >= batch - 1;
+        if (!batch_outer && !token_outer) return BIMAMBA_ERR_INVALID_ARG;
+    }
+    return BIMAMBA_OK;
+}
+
+GlrRows rows(const bimamba_rows_t& q) { return {q.ptr, q.batch_stride, q.token_stride}; }
+
+int check_common(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, int batch, int64_t L, int D,
+                 unsigned flags) {
+    if (!in || !p || !sizes_ok(batch, L, D)) return BIMAMBA_ERR_INVALID_ARG;
+    if (flags & ~BIMAMBA_GLR_REVERSE) return BIMAMBA_ERR_UNSUPPORTED;
+    if (!dtype_ok(in->dtype)) return BIMAMBA_ERR_UNSUPPORTED;
+    const size_t e = elem_size(in->dtype);
+    int rc = check_in(in->x, e, false);
+    if (!rc) rc = check_in(in->r, e, false);
+    if (!rc) rc = check_in(in->i, e, false);
+    if (!rc) rc = check_in(in->add, e, true);
+    if (!rc) rc = check_in(in->z, e, true);
+    if (rc) return rc;
+    if (!p->A) return BIMAMBA_ERR_INVALID_ARG;
+    if (!aligned(p->A, 4) || !aligned(p->r_bias, 4) || !aligned(p->i_bias, 4) || !aligned(in->lengths, 4))
+        return BIMAMBA_ERR_MISALIGNED;
+    return BIMAMBA_OK;
+}
+
+void fill_common(GlrParams& k, const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, int batch, int64_t L,
+                 int D, unsigned flags) {
+    k.x = rows(in->x);
+    k.r = rows(in->r);
+    k.i = rows(in->i);
+    k.add = rows(in->add);
+    k.z = rows(in->z);
+    k.lengths = in->lengths;
+    k.A = p->A;
+    k.r_bias = p->r_bias;
+    k.i_bias = p->i_bias;
+    k.L = L;
+    k.D = D;
+    k.batch = batch;
+    k.reverse = (flags & BIMAMBA_GLR_REVERSE) ? 1 : 0;
+    k.nchunk = (L + bimamba::kGlrChunk - 1) / bimamba::kGlrChunk;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    return !ws || !aligned(ws, 256) || have < need ? BIMAMBA_ERR_WORKSPACE : BIMAMBA_OK;
+}
+
+}  // namespace
+
+namespace bimamba {
+
+int glr_error_word(int, unsigned int* word) {
+    *word = 0;
+    return BIMAMBA_OK;
+}
+
+}  // namespace bimamba
+
+extern "C" {
+
+size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backward) {
+    if (!sizes_ok(batch, L, d_inner)) return 0;
+    return backward ? (size_t)batch * 3 * (size_t)d_inner * sizeof(float) : 256;
+}
+
+int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const float* h_in,
+                    const bimamba_rows_t* out, float* h_out, float* chunk_states, int batch, int64_t L, int d_inner,
+                    unsigned flags, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+    int rc = check_common(in, p, batch, L, d_inner, flags);
+    if (rc) return rc;
+    if (!out) return BIMAMBA_ERR_INVALID_ARG;
+    if ((rc = check_out(*out, elem_size(in->dtype), batch, L, d_inner))) return rc;
+    if (!aligned(h_in, 4) || !aligned(h_out, 4) || !aligned(chunk_states, 4)) return BIMAMBA_ERR_MISALIGNED;
+    if ((rc = check_workspace(workspace, workspace_bytes, bimamba_glr_workspace_bytes(batch, L, d_inner, 0)))) return rc;
+
+    GlrParams k = {};
+    fill_common(k, in, p, batch, L, d_inner, flags);
+    k.out = rows(*out);
+    k.h_in = h_in;
+    k.h_out = h_out;
+    k.chunk = chunk_states;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    const dim3 grid((unsigned)((d_inner + 127) / 128), (unsigned)batch);
+    if (in->dtype == BIMAMBA_BF16)
+        bimamba::glr_fwd_kernel<bf16><<<grid, 128, 0, st>>>(k);
+    else
+        bimamba::glr_fwd_kernel<float><<<grid, 128, 0, st>>>(k);
+    return launch_status();
+}
+
+int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const bimamba_rows_t* dout,
+                    const float* chunk_states, const float* dh_out, const bimamba_glr_grads_t* grads, int batch,
+                    int64_t L, int d_inner, unsigned flags, void* workspace, size_t workspace_bytes,
+                    void* cuda_stream) {
+    int rc = check_common(in, p, batch, L, d_inner, flags);
+    if (rc) return rc;
+    if (!dout || !chunk_states || !grads) return BIMAMBA_ERR_INVALID_ARG;
+    const size_t e = elem_size(in->dtype);
+    if ((rc = check_in(*dout, e, false))) return rc;
+    if ((rc = check_out(grads->dx, e, batch, L, d_inner))) return rc;
+    if ((rc = check_out(grads->dr, e, batch, L, d_inner))) return rc;
+    if ((rc = check_out(grads->di, e, batch, L, d_inner))) return rc;
+    if (in->add.ptr && (rc = check_out(grads->dadd, e, batch, L, d_inner))) return rc;
+    if (in->z.ptr && (rc = check_out(grads->dz, e, batch, L, d_inner))) return rc;
+    if (!aligned(chunk_states, 4) || !aligned(dh_out, 4) || !aligned(grads->dA, 4) || !aligned(grads->dr_bias, 4) ||
+        !aligned(grads->di_bias, 4) || !aligned(grads->dh_in, 4))
+        return BIMAMBA_ERR_MISALIGNED;
+    if ((rc = check_workspace(workspace, workspace_bytes, bimamba_glr_workspace_bytes(batch, L, d_inner, 1)))) return rc;
+
+    GlrParams k = {};
+    fill_common(k, in, p, batch, L, d_inner, flags);
+    k.dout = rows(*dout);
+    k.dx = rows(grads->dx);
+    k.dr = rows(grads->dr);
+    k.di = rows(grads->di);
+    k.dadd = rows(grads->dadd);
+    k.dz = rows(grads->dz);
+    k.chunk = const_cast<float*>(chunk_states);
+    k.dh_out = dh_out;
+    k.dh_in = grads->dh_in;
+    k.part = static_cast<float*>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    const dim3 grid((unsigned)((d_inner + 127) / 128), (unsigned)batch);
+    if (in->dtype == BIMAMBA_BF16)
+        bimamba::glr_bwd_kernel<bf16><<<grid, 128, 0, st>>>(k);
+    else
+        bimamba::glr_bwd_kernel<float><<<grid, 128, 0, st>>>(k);
+    if ((rc = launch_status())) return rc;
+    if (grads->dA || grads->dr_bias || grads->di_bias)
+        bimamba::glr_sums_kernel<<<(unsigned)((3LL * d_inner + 127) / 128), 128, 0, st>>>(
+            k.part, batch, d_inner, grads->dA, grads->dr_bias, grads->di_bias);
+    return launch_status();
+}
+
+}  // extern "C"

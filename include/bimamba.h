@@ -418,6 +418,164 @@ int bimamba_in_proj(const void *a, const void *w_in, int batch, int64_t L, int d
 int bimamba_out_proj(const void *y, const void *w_out, int batch, int64_t L, int d_inner, int d_model, void *out,
                      void *cuda_stream);
 
+/* ---------------------------------------------------------------- gated linear recurrence
+ * One direction of a mixer whose state is one number per channel: a decay
+ * and an input gate from raw activations, then a linear scan.  Beside the
+ * selective scans above it is the cheaper mixer (no conv, no state dimension),
+ * and it has a backward pass, padded batches and strided inputs.  Per batch row
+ * b and channel d, over the row's len tokens in scan order s = 0..len-1
+ * (token t = s, or t = len-1-s with BIMAMBA_GLR_REVERSE):
+ *   rg = sigmoid(r[t] + r_bias[d]),  ig = sigmoid(i[t] + i_bias[d])
+ *   a  = exp(A[d] * rg),             beta = sqrt(1 - a^2)
+ *   h  = a * h + beta * ig * x[t]    from h = h_in[b][d] (or 0)
+ *   out[t] = (h + add[t]) * silu(z[t])      (without add: h; without z: no gate)
+ * and h_out[b][d] = h after the last token.  Two calls make the bidirectional
+ * mixer (§3.2 Eq. (4)-(6): two directions whose outputs are added): the
+ * forward one, then the reverse one with add = the first call's out and the
+ * layer's z.  A call with few tokens, h_in and h_out is the serving form (one new
+ * token, or an active block of them).
+ *   Padded batches: row b has len = lengths[b] tokens (clamped to [0, L]; L
+ * without lengths).  Tokens at and after len are not read, their outputs
+ * (and gradients) are written as 0, and a row of no tokens has h_out = h_in. */
+
+/* Scan the row from its last token to its first. */
+#define BIMAMBA_GLR_REVERSE 0x8u
+/* Tokens between the states that a forward call saves for the backward. */
+#define BIMAMBA_GLR_CHUNK 64
+
+/* Token rows of d_inner elements: element (b, t, d) is at
+ * ptr[b * batch_stride + t * token_stride + d] (strides in elements, >= 0). */
+typedef struct {
+    void *ptr;
+    int64_t batch_stride;
+    int64_t token_stride;
+} bimamba_rows_t;
+
+/* Parameters of the direction, fp32 device pointers. */
+typedef struct {
+    const float *A;       /* [d_inner], <= 0: the log decay of a wide-open gate (a positive entry gives NaN) */
+    const float *r_bias;  /* [d_inner] or NULL (= 0) */
+    const float *i_bias;  /* [d_inner] or NULL (= 0) */
+} bimamba_glr_params_t;
+
+/* Inputs of `dtype` (x, r, i may be column slices of one projection's
+ * output, so that nothing is copied; rows may also be shared with stride 0). */
+typedef struct {
+    bimamba_rows_t x, r, i;
+    bimamba_rows_t add;       /* ptr NULL = none */
+    bimamba_rows_t z;         /* ptr NULL = none */
+    const int32_t *lengths;   /* [batch] device memory, or NULL */
+    bimamba_dtype_t dtype;
+} bimamba_glr_inputs_t;
+
+/* Bytes of device workspace of bimamba_glr_fwd (backward == 0) or
+ * bimamba_glr_bwd (backward != 0); 0 for invalid sizes. */
+size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backward);
+
+/* Forward.
+ *   h_in         [batch][d_inner] fp32 or NULL; h_out may be h_in (in place)
+ *   out          rows of in->dtype; must not overlap an input, nor its own rows one another
+ *   h_out        [batch][d_inner] fp32 or NULL
+ *   chunk_states [batch][ceil(L / BIMAMBA_GLR_CHUNK)][d_inner] fp32 or NULL: the state
+ *                entering each BIMAMBA_GLR_CHUNK steps, which bimamba_glr_bwd needs
+ *                (chunks that start at or after len are left as they were)
+ *   workspace    >= bimamba_glr_workspace_bytes(..., 0) bytes, 256-byte aligned
+ *                (two calls that overlap on the GPU need one each)
+ * flags: BIMAMBA_GLR_REVERSE. */
+int bimamba_glr_fwd(const bimamba_glr_inputs_t *in, const bimamba_glr_params_t *p, const float *h_in,
+                    const bimamba_rows_t *out, float *h_out, float *chunk_states,
+                    int batch, int64_t L, int d_inner, unsigned flags,
+                    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* Gradients: rows of in->dtype (distinct tensors; they may be column slices
+ * of one buffer), and fp32 sums over all tokens (any of them may be NULL). */
+typedef struct {
+    bimamba_rows_t dx, dr, di;
+    bimamba_rows_t dadd;   /* with in->add */
+    bimamba_rows_t dz;     /* with in->z */
+    float *dA;             /* [d_inner] or NULL */
+    float *dr_bias;        /* [d_inner] or NULL */
+    float *di_bias;        /* [d_inner] or NULL */
+    float *dh_in;          /* [batch][d_inner] or NULL: gradient of h_in */
+} bimamba_glr_grads_t;
+
+/* Backward of a bimamba_glr_fwd call with the same inputs, parameters,
+ * lengths and flags.
+ *   dout         rows of in->dtype: gradient of out
+ *   chunk_states as the forward left it
+ *   dh_out       [batch][d_inner] fp32 or NULL: gradient of h_out; dh_in may be dh_out
+ * Where beta is 0 (A = 0, or a gate closed beyond fp32) the derivative of
+ * sqrt(1 - a^2), which is infinite there, is taken as 0.  The result does not
+ * depend on the order in which the GPU runs its blocks (no floating atomics). */
+int bimamba_glr_bwd(const bimamba_glr_inputs_t *in, const bimamba_glr_params_t *p, const bimamba_rows_t *dout,
+                    const float *chunk_states, const float *dh_out, const bimamba_glr_grads_t *grads,
+                    int batch, int64_t L, int d_inner, unsigned flags,
+                    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* ---------------------------------------------------------------- block norm
+ * What stands between two blocks of the denoiser (App. A.1 Eq. (10)-(12)): the
+ * branch joins the residual stream through its gate, and the next block's
+ * norm reads the stream, in one pass.  Per token row of batch row b:
+ *   un    = N(u) * post_w        (without post_w: u)
+ *   x_out = res_scale * x + gate[b] * un     (without u: res_scale * x; without gate: un)
+ *   y     = gamma[b] * N(x_out) + beta[b]    (NULL gamma: 1; NULL beta: 0)
+ * N(v) = (v - mean) / sqrt(variance + eps) over the row's d values, or with
+ * BIMAMBA_NORM_RMS v / sqrt(mean(v^2) + eps).  y is the norm of the stream as
+ * it is stored, rounded to stream_dtype, so that it equals what a separate call on x_out
+ * would give and what the backward differentiates. */
+#define BIMAMBA_NORM_RMS          0x10u  /* both norms are root-mean-square norms */
+#define BIMAMBA_NORM_GATE_SHARED  0x20u  /* gate is one [d] for all batch rows    */
+#define BIMAMBA_NORM_GAMMA_SHARED 0x40u  /* gamma and beta are one [d] for all    */
+
+/* fp32 device pointers; each [batch][d], or [d] with its flag. */
+typedef struct {
+    const float *gate;    /* or NULL (= 1) */
+    const float *post_w;  /* [d] or NULL (the branch is not normed) */
+    const float *gamma;   /* or NULL (= 1) */
+    const float *beta;    /* or NULL (= 0) */
+    float res_scale;
+    float eps;            /* > 0 */
+} bimamba_block_norm_params_t;
+
+/* Forward.  x, x_out [batch][L][d] of stream_dtype (x_out may be x, and may
+ * be NULL: not stored); u, y [batch][L][d] of dtype, either may be NULL (no
+ * branch; the stream alone) but x_out and y not both.  stats [batch][L][4] fp32
+ * or NULL: mean and 1/sigma of x_out's rows, then of u's (0 and 1 where that
+ * norm is absent; a mean is 0 with BIMAMBA_NORM_RMS), for the backward.
+ * Types: (stream, dtype) = bf16/bf16, fp32/bf16 or fp32/fp32 (else
+ * UNSUPPORTED).  d <= 16384 (else UNSUPPORTED).  One kernel launch. */
+int bimamba_block_norm_fwd(const void *x, const void *u, const bimamba_block_norm_params_t *p,
+                           void *x_out, void *y, float *stats,
+                           bimamba_dtype_t stream_dtype, bimamba_dtype_t dtype,
+                           int batch, int64_t L, int d, unsigned flags, void *cuda_stream);
+
+/* Bytes of device workspace bimamba_block_norm_bwd needs; 0 for invalid sizes. */
+size_t bimamba_block_norm_workspace_bytes(int batch, int64_t L, int d);
+
+/* Gradients; any of the vectors may be NULL.  dgate, dgamma, dbeta have the
+ * layouts of gate, gamma, beta (a shared vector's is summed over all rows). */
+typedef struct {
+    void *dx;        /* [batch][L][d] of stream_dtype; may be dx_out (in place) */
+    void *du;        /* [batch][L][d] of dtype; NULL exactly when u is */
+    float *dgate;    /* needs gate   */
+    float *dpost_w;  /* needs post_w, [d] */
+    float *dgamma;   /* needs gamma  */
+    float *dbeta;
+} bimamba_block_norm_grads_t;
+
+/* Backward.  x_out, u, stats: as the forward left them (u NULL without a
+ * branch); dy [batch][L][d] of dtype or NULL (y not used); dx_out
+ * [batch][L][d] of stream_dtype or NULL (the stream is not used after y), not
+ * both NULL.  p->beta and p->eps are not read.  The vectors are summed in a
+ * fixed order (no floating atomics).  workspace: at least
+ * bimamba_block_norm_workspace_bytes() bytes, 256-byte aligned.  One kernel
+ * launch, two where a vector is wanted. */
+int bimamba_block_norm_bwd(const void *dy, const void *dx_out, const void *x_out, const void *u, const float *stats,
+                           const bimamba_block_norm_params_t *p, const bimamba_block_norm_grads_t *grads,
+                           bimamba_dtype_t stream_dtype, bimamba_dtype_t dtype,
+                           int batch, int64_t L, int d, unsigned flags,
+                           void *workspace, size_t workspace_bytes, void *cuda_stream);
+
 /* The per-token features the layer computes before its scans, written out
  * for inspection (a diagnostic: the layer kernels keep them in registers and
  * never store them).  With the definitions at the top of this header:
