@@ -45,7 +45,7 @@ GlrRows rows(const bimamba_rows_t& q) { return {q.ptr, q.batch_stride, q.token_s
 int check_common(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, int batch, int64_t L, int D,
                  unsigned flags) {
     if (!in || !p || !sizes_ok(batch, L, D)) return BIMAMBA_ERR_INVALID_ARG;
-    if (flags & ~BIMAMBA_GLR_REVERSE) return BIMAMBA_ERR_UNSUPPORTED;
+    if (flags & ~(BIMAMBA_GLR_REVERSE | BIMAMBA_TEST_STARVE)) return BIMAMBA_ERR_UNSUPPORTED;
     if (!dtype_ok(in->dtype)) return BIMAMBA_ERR_UNSUPPORTED;
     const size_t e = elem_size(in->dtype);
     int rc = check_in(in->x, e, false);
@@ -86,18 +86,75 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 
 namespace bimamba {
 
-int glr_error_word(int, unsigned int* word) {
-    *word = 0;
+int glr_error_word(int reset, unsigned int* word) {
+    if (cudaMemcpyFromSymbol(word, g_glr_error, sizeof(*word)) != cudaSuccess) return BIMAMBA_ERR_CUDA;
+    const unsigned int zero = 0;
+    if (reset && cudaMemcpyToSymbol(g_glr_error, &zero, sizeof(zero)) != cudaSuccess) return BIMAMBA_ERR_CUDA;
     return BIMAMBA_OK;
 }
 
 }  // namespace bimamba
 
+namespace {
+
+// The smallest tile of a launch (fp32); the workspace is sized for it.
+constexpr int kSmallTile = bimamba::kGlrTok<float> * bimamba::kGlrWarps;
+
+// The hand-over workspace of a launch whose rows have `tiles` tiles: the
+// ticket (256 bytes), the maps, the groups' entering states.
+size_t sync_bytes(int batch, int D, int64_t tiles) {
+    const size_t chains = (size_t)batch * ((D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    const size_t groups = (size_t)(tiles + bimamba::kGlrGroup - 1) / bimamba::kGlrGroup;
+    return 256 + chains * bimamba::kGlrSlab * ((size_t)tiles * 8 + groups * 4);
+}
+
+// Points y at the workspace and enqueues the all-ones fill (a row of one tile
+// hands nothing over and gets neither).
+int make_sync(bimamba::GlrSync& y, int batch, int D, int64_t tiles, unsigned flags, void* ws, cudaStream_t st) {
+    y = {};
+    y.tiles = tiles;
+    y.groups = (tiles + bimamba::kGlrGroup - 1) / bimamba::kGlrGroup;
+    if (tiles <= 1) return BIMAMBA_OK;
+    const size_t chains = (size_t)batch * ((D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    y.starve = (flags & BIMAMBA_TEST_STARVE) ? 1 : 0;
+    y.wait_limit = y.starve ? kStarveWaitCycles : kWaitCycles;
+    unsigned char* q = static_cast<unsigned char*>(ws);
+    y.ticket = reinterpret_cast<unsigned int*>(q);
+    y.map = reinterpret_cast<unsigned long long*>(q + 256);
+    y.state = reinterpret_cast<float*>(q + 256 + chains * bimamba::kGlrSlab * (size_t)tiles * 8);
+    return cudaMemsetAsync(ws, 0xff, sync_bytes(batch, D, tiles), st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
+}
+
+// Pairs of channels in one access: every row of q starts at an even element of a pair-aligned pointer.
+bool paired(const GlrRows& q, size_t esz) {
+    return !q.p || (aligned(q.p, 2 * esz) && q.bs % 2 == 0 && q.ts % 2 == 0);
+}
+
+template <typename T, bool VEC>
+int launch_fwd(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+    constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
+    const int64_t tiles = (k.L + TILE - 1) / TILE;
+    const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
+    const int64_t blocks = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    if (blocks > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
+    bimamba::GlrSync y;
+    int rc = make_sync(y, k.batch, k.D, tiles, flags, ws, st);
+    if (rc) return rc;
+    if (k.add.p || k.z.p)
+        bimamba::glr_tile_fwd_kernel<T, VEC, true><<<(unsigned)blocks, warps * 32, 0, st>>>(k, y);
+    else
+        bimamba::glr_tile_fwd_kernel<T, VEC, false><<<(unsigned)blocks, warps * 32, 0, st>>>(k, y);
+    return launch_status();
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backward) {
     if (!sizes_ok(batch, L, d_inner)) return 0;
-    return backward ? (size_t)batch * 3 * (size_t)d_inner * sizeof(float) : 256;
+    return backward ? (size_t)batch * 3 * (size_t)d_inner * sizeof(float)
+                    : sync_bytes(batch, d_inner, (L + kSmallTile - 1) / kSmallTile);
 }
 
 int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const float* h_in,
@@ -117,12 +174,12 @@ int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     k.h_out = h_out;
     k.chunk = chunk_states;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    const dim3 grid((unsigned)((d_inner + 127) / 128), (unsigned)batch);
+    const size_t e = elem_size(in->dtype);
+    const bool vec = d_inner % 2 == 0 && paired(k.x, e) && paired(k.r, e) && paired(k.i, e) && paired(k.add, e) &&
+                     paired(k.z, e) && paired(k.out, e);
     if (in->dtype == BIMAMBA_BF16)
-        bimamba::glr_fwd_kernel<bf16><<<grid, 128, 0, st>>>(k);
-    else
-        bimamba::glr_fwd_kernel<float><<<grid, 128, 0, st>>>(k);
-    return launch_status();
+        return vec ? launch_fwd<bf16, true>(k, flags, workspace, st) : launch_fwd<bf16, false>(k, flags, workspace, st);
+    return vec ? launch_fwd<float, true>(k, flags, workspace, st) : launch_fwd<float, false>(k, flags, workspace, st);
 }
 
 int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const bimamba_rows_t* dout,
