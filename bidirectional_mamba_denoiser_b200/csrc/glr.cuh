@@ -44,7 +44,7 @@ struct GlrParams {
     float* chunk;          // [batch][nchunk][D]: forward writes (or null), backward reads
     const float* dh_out;   // or null
     float* dh_in;          // or null
-    float* part;           // backward: [batch rows of partial sums][3][D]
+    float* part;           // backward: [batch * nchunk][3][D] partial sums
     int64_t L;
     int D, batch, reverse;
     int64_t nchunk;        // ceil(L / kGlrChunk)
@@ -68,6 +68,13 @@ __device__ __forceinline__ float glr_sqrt(float v) {
     return y;
 }
 
+// 0 for 0 and for what flushes to it, where beta = v * this is 0 as well
+__device__ __forceinline__ float glr_rsqrt(float v) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return v < 1.17549435e-38f ? 0.f : y;
+}
+
 // 1 / (1 + e^-v): e^-v may be +inf, whose reciprocal is 0.
 __device__ __forceinline__ float glr_sigmoid(float v) { return glr_rcp(1.f + glr_ex2(-v * kGlrLog2e)); }
 
@@ -84,31 +91,7 @@ __device__ __forceinline__ float glr_one_minus_a2(float t, float a) {
     return t > -0.25f ? -t * s : fmaf(-a, a, 1.f);
 }
 
-struct GlrGate {
-    float rg, ig, a, b2;  // b2 = beta^2
-};
-
-__device__ __forceinline__ GlrGate glr_gate(float r, float i, float A) {
-    GlrGate g;
-    g.rg = glr_sigmoid(r);
-    g.ig = glr_sigmoid(i);
-    const float la = A * g.rg;
-    g.a = glr_ex2(la * kGlrLog2e);
-    g.b2 = glr_one_minus_a2(2.f * la, g.a);
-    return g;
-}
-
 // ---------------------------------------------------------------- element I/O
-
-template <typename T>
-__device__ __forceinline__ float glr_ld(const GlrRows& q, int64_t b, int64_t t, int d) {
-    const T* p = static_cast<const T*>(q.p) + b * q.bs + t * q.ts + d;
-    return static_cast<float>(*p);
-}
-template <typename T>
-__device__ __forceinline__ void glr_st(const GlrRows& q, int64_t b, int64_t t, int d, float v) {
-    static_cast<T*>(q.p)[b * q.bs + t * q.ts + d] = static_cast<T>(v);  // bf16: to nearest even
-}
 
 __device__ __forceinline__ int64_t glr_len(const GlrParams& p, int64_t b) {
     if (!p.lengths) return p.L;
@@ -451,79 +434,215 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_fwd_kernel(const G
     }
 }
 
-// ---------------------------------------------------------------- one thread per channel
+// Backward, one tile of kGlrChunk steps: the tiles are walked from the last
+// step to the first (tile tj from the end of the row's own tiles), and what
+// they hand over is q = a G, which the affine map of a tile takes from its
+// right end to its left.  A warp's steps share one product P for both
+// scans, the recomputed states (ascending, from the saved state that enters the tile)
+// and q (descending).
+constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
 
-// Chunk by chunk from the last: the states of the chunk from its saved first
-// one, then the gradients from its last step to its first.
-template <typename T>
-__global__ void glr_bwd_kernel(const GlrParams p) {
-    const int d = blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t b = blockIdx.y;
-    if (d >= p.D) return;
-    const int64_t len = glr_len(p, b);
-    const float A = p.A[d], rb = p.r_bias ? p.r_bias[d] : 0.f, ib = p.i_bias ? p.i_bias[d] : 0.f;
-    float q = p.dh_out ? p.dh_out[b * p.D + d] : 0.f;  // a_{s+1} G_{s+1}
-    float sA = 0.f, sr = 0.f, si = 0.f;
-    float hp[kGlrChunk];  // the state before each step
-    for (int64_t c = (len + kGlrChunk - 1) / kGlrChunk - 1; c >= 0; --c) {
-        const int64_t s0 = c * kGlrChunk;
-        const int n = (int)(len - s0 < kGlrChunk ? len - s0 : kGlrChunk);
-        float h = p.chunk[(b * p.nchunk + c) * p.D + d];
-        for (int j = 0; j < n; ++j) {
-            const int64_t t = p.reverse ? len - 1 - (s0 + j) : s0 + j;
-            const GlrGate g = glr_gate(glr_ld<T>(p.r, b, t, d) + rb, glr_ld<T>(p.i, b, t, d) + ib, A);
-            hp[j] = h;
-            h = fmaf(g.a, h, glr_sqrt(g.b2) * g.ig * glr_ld<T>(p.x, b, t, d));
-        }
-        for (int j = n - 1; j >= 0; --j) {
-            const int64_t t = p.reverse ? len - 1 - (s0 + j) : s0 + j;
-            const GlrGate g = glr_gate(glr_ld<T>(p.r, b, t, d) + rb, glr_ld<T>(p.i, b, t, d) + ib, A);
-            const float beta = glr_sqrt(g.b2), bi = beta * g.ig, w = bi * glr_ld<T>(p.x, b, t, d);
-            float dh = glr_ld<T>(p.dout, b, t, d);
-            if (p.add.p || p.z.p) {
-                const float hs = fmaf(g.a, hp[j], w) + (p.add.p ? glr_ld<T>(p.add, b, t, d) : 0.f);
-                if (p.z.p) {
-                    const float z = glr_ld<T>(p.z, b, t, d), sz = glr_sigmoid(z);
-                    glr_st<T>(p.dz, b, t, d, dh * hs * (sz * fmaf(z, 1.f - sz, 1.f)));
-                    dh *= z * sz;
-                }
-                if (p.add.p) glr_st<T>(p.dadd, b, t, d, dh);
+template <typename T, bool VEC, bool EPI>
+__global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_bwd_kernel(const GlrParams p, const GlrSync y) {
+    constexpr int TOK = kGlrBwdTok;
+    __shared__ float2 aggP[kGlrWarps][32], aggh[kGlrWarps][32], aggq[kGlrWarps][32];
+    __shared__ float2 enter[32];
+    __shared__ unsigned ticket;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned id = blockIdx.x;
+    if (y.ticket) {
+        if (threadIdx.x == 0) ticket = atomicAdd(y.ticket, 1u) + 1u;
+        __syncthreads();
+        id = ticket;
+    }
+    const int slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
+    const unsigned chains = (unsigned)slabs * p.batch, rs = id % chains;
+    const int64_t tj = id / chains, b = rs / slabs;
+    const int c0 = (int)(rs % slabs) * kGlrSlab + 2 * lane;
+    const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
+    const int64_t len = glr_len(p, b), used = (len + kGlrChunk - 1) / kGlrChunk;  // the row's own tiles
+    const int64_t ti = tj < used ? used - 1 - tj : tj;
+    const int64_t s0 = ti * kGlrChunk, s1 = s0 + kGlrChunk;
+    float* part = p.part + ((int64_t)b * p.nchunk + ti) * 3 * p.D + c0;
+    if (len < s1) {
+        const int64_t z0 = len > s0 ? len : s0, z1 = s1 < p.L ? s1 : p.L;
+        glr_zero_rows<T, VEC>(p.dx, b, z0, z1, c0, nch, warp, kGlrWarps);
+        glr_zero_rows<T, VEC>(p.dr, b, z0, z1, c0, nch, warp, kGlrWarps);
+        glr_zero_rows<T, VEC>(p.di, b, z0, z1, c0, nch, warp, kGlrWarps);
+        if (EPI && p.add.p) glr_zero_rows<T, VEC>(p.dadd, b, z0, z1, c0, nch, warp, kGlrWarps);
+        if (EPI && p.z.p) glr_zero_rows<T, VEC>(p.dz, b, z0, z1, c0, nch, warp, kGlrWarps);
+    }
+    if (len <= s0) {
+        if (warp < 3) glr_put2(part + (int64_t)warp * p.D, glr_f2(0.f), nch);
+        if (tj == 0 && warp == 0 && p.dh_in)
+            glr_put2(p.dh_in + b * p.D + c0, glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch), nch);
+        return;
+    }
+
+    const int64_t ws = s0 + warp * TOK;
+    const int n = len - ws >= TOK ? TOK : (len > ws ? (int)(len - ws) : 0);
+    const int64_t t0 = p.reverse ? len - 1 - ws : ws;
+    const int step = p.reverse ? -1 : 1;
+    GlrRaw<T> rx[TOK], rd[TOK], ra[EPI ? TOK : 1], rz[EPI ? TOK : 1];
+    float2 rg[TOK], ig[TOK], a[TOK], hp[TOK];
+    const float2 A = glr_vec2(p.A + c0, nch);
+    {
+        GlrRaw<T> rr[TOK], ri[TOK];
+        const T* px = static_cast<const T*>(p.x.p) + b * p.x.bs + t0 * p.x.ts + c0;
+        const T* pr = static_cast<const T*>(p.r.p) + b * p.r.bs + t0 * p.r.ts + c0;
+        const T* pi = static_cast<const T*>(p.i.p) + b * p.i.bs + t0 * p.i.ts + c0;
+        const T* pd = static_cast<const T*>(p.dout.p) + b * p.dout.bs + t0 * p.dout.ts + c0;
+        const int64_t ax = step * p.x.ts, ar = step * p.r.ts, ai = step * p.i.ts, ad = step * p.dout.ts;
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const int m = j < n ? nch : 0;
+            rx[j] = glr_ld2<VEC>(px + j * ax, m);
+            rr[j] = glr_ld2<VEC>(pr + j * ar, m);
+            ri[j] = glr_ld2<VEC>(pi + j * ai, m);
+            rd[j] = glr_ld2<VEC>(pd + j * ad, m);
+            if constexpr (EPI) {
+                const int64_t t = t0 + step * j;
+                ra[j] = glr_ld2<VEC>(static_cast<const T*>(p.add.p) + b * p.add.bs + t * p.add.ts + c0, p.add.p ? m : 0);
+                rz[j] = glr_ld2<VEC>(static_cast<const T*>(p.z.p) + b * p.z.bs + t * p.z.ts + c0, p.z.p ? m : 0);
             }
-            const float G = dh + q;
-            const float ratio = beta > 0.f ? g.a * g.a * glr_rcp(g.b2) : 0.f;  // beta is 0 for a denormal b2 too
-            const float dla = G * fmaf(g.a, hp[j], -ratio * w);
-            const float dr = A * dla * g.rg * (1.f - g.rg), di = G * w * (1.f - g.ig);
-            glr_st<T>(p.dx, b, t, d, G * bi);
-            glr_st<T>(p.dr, b, t, d, dr);
-            glr_st<T>(p.di, b, t, d, di);
-            sA = fmaf(g.rg, dla, sA);
-            sr += dr;
-            si += di;
-            q = g.a * G;
+        }
+        const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+        const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+        float2 P = glr_f2(1.f), h = glr_f2(0.f);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const GlrGate2 g = glr_gate2(rr[j].get(), ri[j].get(), nr, ni, A);
+            const float2 beta = make_float2(glr_sqrt(g.b2.x), glr_sqrt(g.b2.y));
+            float2 w = glr_mul(glr_mul(beta, g.ig), rx[j].get());
+            rg[j] = g.rg;
+            ig[j] = g.ig;
+            a[j] = g.a;
+            if (j >= n) a[j] = glr_f2(1.f), w = glr_f2(0.f);
+            hp[j] = h;  // the state before step j, from a zero state at the warp's first
+            P = glr_mul(P, a[j]);
+            h = glr_fma(a[j], h, w);
+        }
+        float2 q = glr_f2(0.f);
+#pragma unroll
+        for (int j = TOK - 1; j >= 0; --j) {
+            float2 dh = rd[j].get();
+            if constexpr (EPI) {
+                if (p.z.p) dh = glr_mul(dh, glr_mul(rz[j].get(), glr_sigmoid2(rz[j].get())));
+            }
+            q = glr_mul(a[j], glr_add(q, dh));  // past the end dout reads as 0 and a is 1
+        }
+        aggP[warp][lane] = P;
+        aggh[warp][lane] = h;
+        aggq[warp][lane] = q;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        float2 P = glr_f2(1.f), q = glr_f2(0.f);
+        for (int w = kGlrWarps - 1; w >= 0; --w) {
+            P = glr_mul(P, aggP[w][lane]);
+            q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
+        }
+        const bool last = ti == 0, publish = y.ticket && !last && !y.starve;
+        unsigned long long* map = y.map + (int64_t)rs * y.tiles * kGlrSlab + 2 * lane;
+        float* state = y.state + (int64_t)rs * y.groups * kGlrSlab + 2 * lane;
+        if (publish) glr_publish_map(map + tj * kGlrSlab, P, q);
+        float2 c;
+        if (tj == 0) {
+            c = glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch);
+            if (publish) glr_publish_state(state, c);
+        } else {
+            c = glr_lookback(y, map, state, tj);
+        }
+        enter[lane] = c;
+        const float2 end = glr_fma(P, c, q);
+        if (publish && (tj + 1) % kGlrGroup == 0) glr_publish_state(state + (tj + 1) / kGlrGroup * kGlrSlab, end);
+        if (last && p.dh_in) glr_put2(p.dh_in + b * p.D + c0, end, nch);
+    }
+    {
+        // the states before the warp's steps, from the one that enters the tile
+        float2 c = glr_vec2(p.chunk + (b * p.nchunk + ti) * p.D + c0, nch);
+        for (int w = 0; w < warp; ++w) c = glr_fma(aggP[w][lane], c, aggh[w][lane]);
+        float2 P = c;
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            hp[j] = glr_add(P, hp[j]);
+            P = glr_mul(P, a[j]);
         }
     }
-    for (int64_t t = len; t < p.L; ++t) {
-        glr_st<T>(p.dx, b, t, d, 0.f);
-        glr_st<T>(p.dr, b, t, d, 0.f);
-        glr_st<T>(p.di, b, t, d, 0.f);
-        if (p.add.p) glr_st<T>(p.dadd, b, t, d, 0.f);
-        if (p.z.p) glr_st<T>(p.dz, b, t, d, 0.f);
+    __syncthreads();
+    float2 q = enter[lane];
+    for (int w = kGlrWarps - 1; w > warp; --w) q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
+    __syncthreads();  // the maps are read: their place takes the sums below
+    float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
+    const float2 one = glr_f2(1.f);
+#pragma unroll
+    for (int j = TOK - 1; j >= 0; --j) {
+        const int m = j < n ? nch : 0;
+        const int64_t t = t0 + step * j;
+        const float2 la = glr_mul(A, rg[j]), t2 = glr_add(la, la);
+        const float2 b2 = make_float2(glr_one_minus_a2(t2.x, a[j].x), glr_one_minus_a2(t2.y, a[j].y));
+        const float2 rs2 = make_float2(glr_rsqrt(b2.x), glr_rsqrt(b2.y));
+        const float2 bi = glr_mul(glr_mul(b2, rs2), ig[j]), w = glr_mul(bi, rx[j].get());
+        float2 dh = rd[j].get();
+        if constexpr (EPI) {
+            if (p.z.p) {
+                const float2 z = rz[j].get(), sz = glr_sigmoid2(z);
+                const float2 h = glr_add(glr_fma(a[j], hp[j], w), ra[j].get());
+                // silu'(z) = s (1 + z (1 - s))
+                const float2 ds = glr_mul(sz, glr_fma(z, glr_fma(sz, glr_f2(-1.f), one), one));
+                glr_st2<VEC>(static_cast<T*>(p.dz.p) + b * p.dz.bs + t * p.dz.ts + c0, glr_mul(glr_mul(dh, h), ds), m);
+                dh = glr_mul(dh, glr_mul(z, sz));
+            }
+            if (p.add.p) glr_st2<VEC>(static_cast<T*>(p.dadd.p) + b * p.dadd.bs + t * p.dadd.ts + c0, dh, m);
+        }
+        const float2 G = glr_add(dh, q);
+        q = glr_mul(a[j], G);
+        // (a / beta)^2 w, with beta = 0 giving 0 (its 1/beta below is then 0 too)
+        const float2 ar = glr_mul(a[j], rs2);
+        const float2 dla = glr_mul(G, glr_fma(a[j], hp[j], glr_mul(glr_mul(ar, ar), glr_mul(w, glr_f2(-1.f)))));
+        const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_fma(rg[j], glr_f2(-1.f), one)));
+        const float2 di = glr_mul(glr_mul(G, w), glr_fma(ig[j], glr_f2(-1.f), one));
+        glr_st2<VEC>(static_cast<T*>(p.dx.p) + b * p.dx.bs + t * p.dx.ts + c0, glr_mul(G, bi), m);
+        glr_st2<VEC>(static_cast<T*>(p.dr.p) + b * p.dr.bs + t * p.dr.ts + c0, dr, m);
+        glr_st2<VEC>(static_cast<T*>(p.di.p) + b * p.di.bs + t * p.di.ts + c0, di, m);
+        if (j < n) {
+            sA = glr_fma(rg[j], dla, sA);
+            sr = glr_add(sr, dr);
+            si = glr_add(si, di);
+        }
     }
-    if (p.dh_in) p.dh_in[b * p.D + d] = q;
-    float* part = p.part + b * 3 * p.D + d;
-    part[0] = sA;
-    part[p.D] = sr;
-    part[2 * p.D] = si;
+    aggP[warp][lane] = sA;
+    aggh[warp][lane] = sr;
+    aggq[warp][lane] = si;
+    __syncthreads();
+    if (warp < 3) {
+        const float2(*from)[32] = warp == 0 ? aggP : (warp == 1 ? aggh : aggq);
+        float2 v = glr_f2(0.f);
+        for (int w = 0; w < kGlrWarps; ++w) v = glr_add(v, from[w][lane]);
+        glr_put2(part + (int64_t)warp * p.D, v, nch);
+    }
 }
 
-// The three sums over the partial rows [n][3][D], in row order.
-__global__ void glr_sums_kernel(const float* part, int64_t n, int D, float* dA, float* dr_bias, float* di_bias) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= 3 * D) return;
+// The three sums over the partial rows [n][3][D]: a block takes 32 columns, each
+// of its 32 warps every 32nd row, and the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) glr_sums_kernel(const float* part, int64_t n, int D, float* dA, float* dr_bias,
+                                                        float* di_bias) {
+    __shared__ float sum[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane, wide = 3LL * D;
     float s = 0.f;
-    for (int64_t k = 0; k < n; ++k) s += part[k * 3 * D + c];
-    float* to = c < D ? dA : (c < 2 * D ? dr_bias : di_bias);
-    if (to) to[c % D] = s;
+    if (c < wide) {
+#pragma unroll 4
+        for (int64_t k = warp; k < n; k += 32) s += part[k * wide + c];
+    }
+    sum[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < wide) {
+        float v = 0.f;
+        for (int w = 0; w < 32; ++w) v += sum[w][lane];
+        float* to = c < D ? dA : (c < 2LL * D ? dr_bias : di_bias);
+        if (to) to[c % D] = v;
+    }
 }
 
 }  // namespace bimamba

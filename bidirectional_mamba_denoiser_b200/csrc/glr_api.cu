@@ -99,6 +99,7 @@ namespace {
 
 // The smallest tile of a launch (fp32); the workspace is sized for it.
 constexpr int kSmallTile = bimamba::kGlrTok<float> * bimamba::kGlrWarps;
+static_assert(kSmallTile <= bimamba::kGlrChunk, "the backward's tiles are no smaller");
 
 // The hand-over workspace of a launch whose rows have `tiles` tiles: the
 // ticket (256 bytes), the maps, the groups' entering states.
@@ -147,14 +148,34 @@ int launch_fwd(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     return launch_status();
 }
 
+template <typename T, bool VEC>
+int launch_bwd(const GlrParams& k, unsigned flags, void* sync, cudaStream_t st) {
+    const int64_t blocks = k.nchunk * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    if (blocks > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
+    bimamba::GlrSync y;
+    int rc = make_sync(y, k.batch, k.D, k.nchunk, flags, sync, st);
+    if (rc) return rc;
+    if (k.add.p || k.z.p)
+        bimamba::glr_tile_bwd_kernel<T, VEC, true><<<(unsigned)blocks, bimamba::kGlrWarps * 32, 0, st>>>(k, y);
+    else
+        bimamba::glr_tile_bwd_kernel<T, VEC, false><<<(unsigned)blocks, bimamba::kGlrWarps * 32, 0, st>>>(k, y);
+    return launch_status();
+}
+
+// The backward's partial sums, one row of 3 D per chunk, in whole 256 bytes.
+size_t part_bytes(int batch, int64_t L, int D) {
+    const size_t rows = (size_t)batch * (size_t)((L + bimamba::kGlrChunk - 1) / bimamba::kGlrChunk);
+    return (rows * 3 * (size_t)D * sizeof(float) + 255) / 256 * 256;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backward) {
     if (!sizes_ok(batch, L, d_inner)) return 0;
-    return backward ? (size_t)batch * 3 * (size_t)d_inner * sizeof(float)
-                    : sync_bytes(batch, d_inner, (L + kSmallTile - 1) / kSmallTile);
+    const size_t sync = sync_bytes(batch, d_inner, (L + kSmallTile - 1) / kSmallTile);
+    return backward ? part_bytes(batch, L, d_inner) + sync : sync;
 }
 
 int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const float* h_in,
@@ -213,16 +234,18 @@ int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     k.dh_out = dh_out;
     k.dh_in = grads->dh_in;
     k.part = static_cast<float*>(workspace);
+    unsigned char* sync = static_cast<unsigned char*>(workspace) + part_bytes(batch, L, d_inner);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    const dim3 grid((unsigned)((d_inner + 127) / 128), (unsigned)batch);
+    const bool vec = d_inner % 2 == 0 && paired(k.x, e) && paired(k.r, e) && paired(k.i, e) && paired(k.add, e) &&
+                     paired(k.z, e) && paired(k.dout, e) && paired(k.dx, e) && paired(k.dr, e) && paired(k.di, e) &&
+                     (!k.add.p || paired(k.dadd, e)) && (!k.z.p || paired(k.dz, e));
     if (in->dtype == BIMAMBA_BF16)
-        bimamba::glr_bwd_kernel<bf16><<<grid, 128, 0, st>>>(k);
+        rc = vec ? launch_bwd<bf16, true>(k, flags, sync, st) : launch_bwd<bf16, false>(k, flags, sync, st);
     else
-        bimamba::glr_bwd_kernel<float><<<grid, 128, 0, st>>>(k);
-    if ((rc = launch_status())) return rc;
-    if (grads->dA || grads->dr_bias || grads->di_bias)
-        bimamba::glr_sums_kernel<<<(unsigned)((3LL * d_inner + 127) / 128), 128, 0, st>>>(
-            k.part, batch, d_inner, grads->dA, grads->dr_bias, grads->di_bias);
+        rc = vec ? launch_bwd<float, true>(k, flags, sync, st) : launch_bwd<float, false>(k, flags, sync, st);
+    if (rc || !(grads->dA || grads->dr_bias || grads->di_bias)) return rc;
+    bimamba::glr_sums_kernel<<<(unsigned)((3LL * d_inner + 31) / 32), 1024, 0, st>>>(
+        k.part, batch * k.nchunk, d_inner, grads->dA, grads->dr_bias, grads->di_bias);
     return launch_status();
 }
 
