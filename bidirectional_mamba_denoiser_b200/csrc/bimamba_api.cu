@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
-#include <set>
 #include <type_traits>
 #include <utility>
 
@@ -39,21 +37,6 @@ constexpr int kWPB = 8;      // warps per CTA (prefix, block step)
 #endif
 constexpr int kPrefixGroup = BIMAMBA_PREFIX_GROUP;
 constexpr int kTBlock = 64;  // longest block of the block step
-
-// Raise the dynamic shared-memory limit of a kernel once per device.
-int ensure_smem(const void* fn, size_t bytes) {
-    if (bytes <= 48 * 1024) return BIMAMBA_OK;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return BIMAMBA_ERR_CUDA;
-    static std::mutex mu;
-    static std::set<std::pair<const void*, int>> done;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({fn, dev})) return BIMAMBA_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return BIMAMBA_ERR_CUDA;
-    done.insert({fn, dev});
-    return BIMAMBA_OK;
-}
 
 // Lanes per channel: the smallest power of two that gives about one resident
 // thread slot per SM thread (148 SMs x 1024), at most 8.

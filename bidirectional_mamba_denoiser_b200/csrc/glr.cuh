@@ -21,6 +21,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "tma_util.cuh"
+
 namespace bimamba {
 
 constexpr int kGlrChunk = 64;
@@ -47,6 +49,7 @@ struct GlrParams {
     float* part;           // backward: [batch * nchunk][3][D] partial sums
     int64_t L;
     int D, batch, reverse;
+    int copy;              // bytes of one asynchronous copy: 16, a pair of elements, or 0 (none possible)
     int64_t nchunk;        // ceil(L / kGlrChunk)
 };
 
@@ -62,34 +65,20 @@ __device__ __forceinline__ float glr_rcp(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
 }
-__device__ __forceinline__ float glr_sqrt(float v) {
-    float y;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-    return y;
-}
-
-// 0 for 0 and for what flushes to it, where beta = v * this is 0 as well
 __device__ __forceinline__ float glr_rsqrt(float v) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-    return v < 1.17549435e-38f ? 0.f : y;
+    return y;
+}
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float glr_max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 
 // 1 / (1 + e^-v): e^-v may be +inf, whose reciprocal is 0.
 __device__ __forceinline__ float glr_sigmoid(float v) { return glr_rcp(1.f + glr_ex2(-v * kGlrLog2e)); }
-
-// 1 - a^2 = -expm1(t), t = 2 la <= 0, a = e^la.  Near 0 the difference would
-// cancel, so down to t = -1/4 the Taylor series of expm1 to t^6 is taken (first
-// omitted term t^6 / 5040 of the sum: 4.8e-8 at most); below, a^2 <= 0.78 and
-// the subtraction loses two bits at most.
-__device__ __forceinline__ float glr_one_minus_a2(float t, float a) {
-    float s = fmaf(t, 1.f / 720.f, 1.f / 120.f);
-    s = fmaf(t, s, 1.f / 24.f);
-    s = fmaf(t, s, 1.f / 6.f);
-    s = fmaf(t, s, 0.5f);
-    s = fmaf(t, s, 1.f);
-    return t > -0.25f ? -t * s : fmaf(-a, a, 1.f);
-}
 
 // ---------------------------------------------------------------- element I/O
 
@@ -181,41 +170,62 @@ __device__ __forceinline__ void glr_put2(float* p, float2 v, int n) {
 
 __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(glr_sigmoid(v.x), glr_sigmoid(v.y)); }
 
+// u = 1 - 2^l for l <= 0, to fp32's relative accuracy however small |l| is, on
+// the FP32 pipe (the special-function unit is the forward's scarcest): l =
+// n + f with |f| <= 1/2 (n by adding and subtracting 1.5 2^23), 2^f - 1 = f p(f)
+// with p of degree 5 (minimax of the relative error by Remez exchange, 1.1e-8),
+// and u = (1 - 2^n) - 2^n (2^f - 1), where 1 - 2^n is exact or far from
+// cancelling.  Below l = -126 the power is as good as 0.
+__device__ __forceinline__ float2 glr_one_minus_ex2(float2 l) {
+    constexpr float kMagic = 12582912.f;
+    l = make_float2(glr_max_nan(l.x, -126.f), glr_max_nan(l.y, -126.f));
+    const float2 m = glr_add(l, glr_f2(kMagic));
+    const float2 f = glr_fma(glr_add(m, glr_f2(-kMagic)), glr_f2(-1.f), l);
+    float2 q = glr_fma(f, glr_f2(0.00015403512225020677f), glr_f2(0.0013390735257416964f));
+    q = glr_fma(f, q, glr_f2(0.009618237614631653f));
+    q = glr_fma(f, q, glr_f2(0.05550357326865196f));
+    q = glr_fma(f, q, glr_f2(0.24022649228572845f));
+    q = glr_fma(f, q, glr_f2(0.6931471824645996f));
+    q = glr_mul(f, q);
+    // -2^n, its exponent from the low bits of m
+    const float2 s = make_float2(__uint_as_float((__float_as_uint(m.x) << 23) + 0xbf800000u),
+                                 __uint_as_float((__float_as_uint(m.y) << 23) + 0xbf800000u));
+    return glr_fma(q, s, glr_add(s, glr_f2(1.f)));
+}
+
+// The gates of a pair: r, i raw activations; nr, ni: -bias log2 e; A2: A log2 e.
 struct GlrGate2 {
-    float2 rg, ig, a, b2;
+    float2 rg, u, a, b2, di;  // a = 1 - u, b2 = beta^2 = 1 - a^2 = u (1 + a), ig = 1 / di
 };
-// r, i: raw activations; nr, ni: -bias log2 e.
-__device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 A) {
+__device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 A2) {
     GlrGate2 g;
     const float2 er = glr_fma(r, glr_f2(-kGlrLog2e), nr), ei = glr_fma(i, glr_f2(-kGlrLog2e), ni);
     const float2 dr = glr_add(make_float2(glr_ex2(er.x), glr_ex2(er.y)), glr_f2(1.f));
-    const float2 di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), glr_f2(1.f));
+    g.di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), glr_f2(1.f));
     g.rg = make_float2(glr_rcp(dr.x), glr_rcp(dr.y));
-    g.ig = make_float2(glr_rcp(di.x), glr_rcp(di.y));
-    const float2 la = glr_mul(A, g.rg), l2 = glr_mul(la, glr_f2(kGlrLog2e));
-    g.a = make_float2(glr_ex2(l2.x), glr_ex2(l2.y));
-    // glr_one_minus_a2, packed
-    const float2 t = glr_add(la, la);
-    float2 s = glr_fma(t, glr_f2(1.f / 720.f), glr_f2(1.f / 120.f));
-    s = glr_fma(t, s, glr_f2(1.f / 24.f));
-    s = glr_fma(t, s, glr_f2(1.f / 6.f));
-    s = glr_fma(t, s, glr_f2(0.5f));
-    s = glr_fma(t, s, glr_f2(1.f));
-    const float2 mt = glr_mul(t, glr_f2(-1.f));
-    const float2 near0 = glr_mul(mt, s), far = glr_fma(glr_mul(g.a, glr_f2(-1.f)), g.a, glr_f2(1.f));
-    g.b2 = make_float2(t.x > -0.25f ? near0.x : far.x, t.y > -0.25f ? near0.y : far.y);
+    g.u = glr_one_minus_ex2(glr_mul(A2, g.rg));
+    g.a = glr_fma(g.u, glr_f2(-1.f), glr_f2(1.f));
+    g.b2 = glr_mul(g.u, glr_add(g.a, glr_f2(1.f)));
     return g;
+}
+// The smallest normal, added under every 1 / beta: 0 / 0 becomes 0, and down to
+// beta^2 = 1e-31 nothing else changes.
+constexpr float kGlrTiny = 1.17549435e-38f;
+// beta ig with one special function: b2 / sqrt(b2 di^2) = sqrt(b2) / di (where
+// di^2 overflows, an input gate below e^-44, it counts as closed).
+__device__ __forceinline__ float2 glr_beta_ig(float2 b2, float2 di) {
+    const float2 v = glr_mul(glr_mul(glr_add(b2, glr_f2(kGlrTiny)), di), di);
+    return glr_mul(b2, make_float2(glr_rsqrt(v.x), glr_rsqrt(v.y)));
 }
 
 // ---------------------------------------------------------------- tiles in scan order
 
-// A block scans one tile: 64 channels (a lane has two) of NW warps x TOK
-// steps.  Each warp scans its TOK steps from a zero state and keeps, per
+// A block scans one tile at a time: 64 channels (a lane has two) of 8 warps x
+// TOK steps.  Each warp scans its TOK steps from a zero state and keeps, per
 // step, the decay since its first step and the state; the warps' affine maps
 // (P, h) meet in shared memory, and with the state that enters the tile every
-// output is P * state + h.  So the inputs are read once, all of a warp's
-// loads are in flight together, and the chain over the sequence is one
-// product-and-add per tile.
+// output is P * state + h.  So the inputs are read once, and the chain over
+// the sequence is one product-and-add per tile.
 //
 // Tiles of one row and channel slab hand over through the workspace, in groups
 // of kGlrGroup: every tile publishes its map; the last of a group also
@@ -225,8 +235,15 @@ __device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, flo
 // only one hop in kGlrGroup waits on another tile's wait.  A published pair is one
 // 64-bit word (or a float each), written once over an all-ones fill that no
 // result has (a NaN of that pattern is replaced), so it needs no flag and no
-// fence.  Tiles are taken in ticket order, so whatever a tile waits for has
-// started; every wait is bounded.
+// fence.  Tiles are taken in ticket order and a block works through its own in
+// that order, so whatever a tile waits for is being worked on; every wait is
+// bounded, and once one has run out the launch's other waits end as well.
+//
+// Blocks stay (as many as the GPU holds) and take the next tile's ticket while
+// they work on one.  Each warp copies the rows of its own steps into its own
+// part of shared memory (cp.async, 16 bytes a lane), NS tiles ahead, so the
+// copies overlap the arithmetic without a barrier: a warp waits for its own
+// copies only.
 constexpr int kGlrSlab = 64;
 constexpr int kGlrGroup = 8;
 constexpr unsigned kGlrErrTimeout = 4u;  // a wait for an earlier tile gave up
@@ -234,10 +251,12 @@ constexpr unsigned kGlrErrTimeout = 4u;  // a wait for an earlier tile gave up
 static __device__ unsigned int g_glr_error;
 
 struct GlrSync {
-    unsigned int* ticket;        // all ones before the launch; null: one tile a row, nothing to hand over
+    unsigned int* ticket;        // [0] the tickets, [1] set once a wait ran out; all ones before the launch.
+                                 // Null: one tile a row, nothing to hand over
     unsigned long long* map;     // [batch * slabs][tiles][64]: (P, h) of each channel
     float* state;                // [batch * slabs][groups][64]: state entering each group
     int64_t tiles, groups;
+    unsigned total;              // tiles of all rows and slabs
     long long wait_limit;
     int starve;                  // test aid: publish nothing
 };
@@ -283,7 +302,11 @@ __device__ __forceinline__ float2 glr_lookback(const GlrSync& y, const unsigned 
             // P lies in [0, 1] (or is NaN, 0x7fffffff): never the fill
             ready = ready && (unsigned)m[k][0] != 0xffffffffu && (unsigned)m[k][1] != 0xffffffffu;
         }
-        if (!ready && clock64() - t0 > y.wait_limit) {
+        if (ready) break;
+        unsigned gone;
+        asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(gone) : "l"(y.ticket + 1) : "memory");
+        if (gone == 0u || clock64() - t0 > y.wait_limit) {
+            atomicExch(y.ticket + 1, 0u);
             atomicOr(&g_glr_error, kGlrErrTimeout);
             break;
         }
@@ -313,314 +336,454 @@ __device__ __forceinline__ void glr_zero_rows(const GlrRows& q, int64_t b, int64
         glr_st2<VEC>(static_cast<T*>(q.p) + b * q.bs + t * q.ts + c0, make_float2(0.f, 0.f), nch);
 }
 
-template <typename T, bool VEC, bool EPI>
-__global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_fwd_kernel(const GlrParams p, const GlrSync y) {
-    constexpr int TOK = kGlrTok<T>;
-    __shared__ float4 agg[kGlrWarps][32];
-    __shared__ float2 enter[32];
-    __shared__ unsigned ticket;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
-    unsigned id = blockIdx.x;
-    if (y.ticket) {
-        if (threadIdx.x == 0) ticket = atomicAdd(y.ticket, 1u) + 1u;
-        __syncthreads();
-        id = ticket;
-    }
-    const int slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
-    const unsigned chains = (unsigned)slabs * p.batch, rs = id % chains;
-    const int64_t ti = id / chains, b = rs / slabs;
-    const int c0 = (int)(rs % slabs) * kGlrSlab + 2 * lane;
-    const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
-    const int64_t len = glr_len(p, b), s0 = ti * (nwarp * TOK);
-    const int64_t s1 = s0 + nwarp * TOK;  // the tile's steps [s0, s1)
-    if (len < s1) glr_zero_rows<T, VEC>(p.out, b, len > s0 ? len : s0, s1 < p.L ? s1 : p.L, c0, nch, warp, nwarp);
-    if (len <= s0) {  // nothing to scan, and no later tile of this row has anything either
-        if (ti == 0 && warp == 0 && p.h_out)
-            glr_put2(p.h_out + b * p.D + c0, glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch), nch);
-        return;
-    }
-
-    const int64_t ws = s0 + warp * TOK;
-    const int n = len - ws >= TOK ? TOK : (len > ws ? (int)(len - ws) : 0);
-    const int64_t t0 = p.reverse ? len - 1 - ws : ws;  // the token of the warp's first step
-    const int step = p.reverse ? -1 : 1;
-    float2 Ps[TOK], hs[TOK];
-    {
-        GlrRaw<T> rx[TOK], rr[TOK], ri[TOK];
-        const T* px = static_cast<const T*>(p.x.p) + b * p.x.bs + t0 * p.x.ts + c0;
-        const T* pr = static_cast<const T*>(p.r.p) + b * p.r.bs + t0 * p.r.ts + c0;
-        const T* pi = static_cast<const T*>(p.i.p) + b * p.i.bs + t0 * p.i.ts + c0;
-        const int64_t ax = step * p.x.ts, ar = step * p.r.ts, ai = step * p.i.ts;
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const int m = j < n ? nch : 0;
-            rx[j] = glr_ld2<VEC>(px + j * ax, m);
-            rr[j] = glr_ld2<VEC>(pr + j * ar, m);
-            ri[j] = glr_ld2<VEC>(pi + j * ai, m);
-        }
-        const float2 A = glr_vec2(p.A + c0, nch);
-        const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-        const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-        float2 P = glr_f2(1.f), h = glr_f2(0.f);
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const GlrGate2 g = glr_gate2(rr[j].get(), ri[j].get(), nr, ni, A);
-            const float2 beta = make_float2(glr_sqrt(g.b2.x), glr_sqrt(g.b2.y));
-            float2 a = g.a, w = glr_mul(glr_mul(beta, g.ig), rx[j].get());
-            if (j >= n) a = glr_f2(1.f), w = glr_f2(0.f);  // past the end: the state stays
-            P = glr_mul(P, a);
-            h = glr_fma(a, h, w);
-            Ps[j] = P;
-            hs[j] = h;
-        }
-        agg[warp][lane] = make_float4(P.x, h.x, P.y, h.y);
-    }
-    GlrRaw<T> ra[EPI ? TOK : 1], rz[EPI ? TOK : 1];
-    if constexpr (EPI) {
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const int m = j < n ? nch : 0;
-            const int64_t t = t0 + step * j;
-            ra[j] = glr_ld2<VEC>(static_cast<const T*>(p.add.p) + b * p.add.bs + t * p.add.ts + c0, p.add.p ? m : 0);
-            rz[j] = glr_ld2<VEC>(static_cast<const T*>(p.z.p) + b * p.z.bs + t * p.z.ts + c0, p.z.p ? m : 0);
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float2 P = glr_f2(1.f), h = glr_f2(0.f);
-        for (int w = 0; w < nwarp; ++w) {
-            const float4 q = agg[w][lane];
-            const float2 Pw = make_float2(q.x, q.z);
-            P = glr_mul(P, Pw);
-            h = glr_fma(Pw, h, make_float2(q.y, q.w));
-        }
-        const bool last = s1 >= len, publish = y.ticket && !last && !y.starve;
-        unsigned long long* map = y.map + (int64_t)rs * y.tiles * kGlrSlab + 2 * lane;
-        float* state = y.state + (int64_t)rs * y.groups * kGlrSlab + 2 * lane;
-        if (publish) glr_publish_map(map + ti * kGlrSlab, P, h);
-        float2 c;
-        if (ti == 0) {
-            // the other tiles take it from here, not from h_in, which may be h_out
-            c = glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch);
-            if (publish) glr_publish_state(state, c);
-        } else {
-            c = glr_lookback(y, map, state, ti);
-        }
-        enter[lane] = c;
-        const float2 end = glr_fma(P, c, h);
-        if (publish && (ti + 1) % kGlrGroup == 0) glr_publish_state(state + (ti + 1) / kGlrGroup * kGlrSlab, end);
-        if (last && p.h_out) glr_put2(p.h_out + b * p.D + c0, end, nch);
-    }
-    __syncthreads();
-    float2 c = enter[lane];
-    for (int w = 0; w < warp; ++w) {
-        const float4 q = agg[w][lane];
-        c = glr_fma(make_float2(q.x, q.z), c, make_float2(q.y, q.w));
-    }
-    if (p.chunk && n > 0 && ws % kGlrChunk == 0) glr_put2(p.chunk + (b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
-    T* po = static_cast<T*>(p.out.p) + b * p.out.bs + t0 * p.out.ts + c0;
-    const int64_t ao = step * p.out.ts;
-#pragma unroll
-    for (int j = 0; j < TOK; ++j) {
-        float2 h = glr_fma(Ps[j], c, hs[j]);
-        if constexpr (EPI) {
-            h = glr_add(h, ra[j].get());
-            if (p.z.p) {
-                const float2 z = rz[j].get();
-                h = glr_mul(h, glr_mul(z, glr_sigmoid2(z)));
-            }
-        }
-        glr_st2<VEC>(po + j * ao, h, j < n ? nch : 0);
-    }
+// Where a tile lies.  `at` counts tiles along the row in the order in which
+// they are walked.
+struct GlrTile {
+    unsigned rs;     // row * slabs + slab
+    int64_t at, b, len;
+    int c;           // first channel
+};
+__device__ __forceinline__ GlrTile glr_tile(const GlrParams& p, unsigned id) {
+    const unsigned slabs = (unsigned)(p.D + kGlrSlab - 1) / kGlrSlab, chains = slabs * (unsigned)p.batch;
+    GlrTile t;
+    t.at = id / chains;
+    t.rs = id % chains;
+    t.b = t.rs / slabs;
+    t.c = (int)(t.rs % slabs) * kGlrSlab;
+    t.len = glr_len(p, t.b);
+    return t;
+}
+// Steps of a row of `len` that start at ws, at most `most`.
+__device__ __forceinline__ int glr_steps(int64_t len, int64_t ws, int most) {
+    return len - ws >= most ? most : (len > ws ? (int)(len - ws) : 0);
 }
 
-// Backward, one tile of kGlrChunk steps: the tiles are walked from the last
-// step to the first (tile tj from the end of the row's own tiles), and what
-// they hand over is q = a G, which the affine map of a tile takes from its
-// right end to its left.  A warp's steps share one product P for both
-// scans, the recomputed states (ascending, from the saved state that enters the tile)
-// and q (descending).
+// A warp's copy of n rows (of TOK) of one tensor into its place: row j is the
+// token t0 + step * j.  The widest copies that the launch found possible;
+// what lies past n or past the last channel becomes 0.
+template <typename T, int TOK>
+__device__ __forceinline__ void glr_copy_rows(T* to, const GlrRows& q, const GlrTile& t, int64_t t0, int step, int n,
+                                              int D, int bytes) {
+    const int lane = threadIdx.x & 31, left = D - t.c;
+    const T* from = static_cast<const T*>(q.p) + t.b * q.bs + t0 * q.ts + t.c;
+    const int64_t ts = step * q.ts;
+    if (bytes == 16) {
+        constexpr int E = 16 / sizeof(T), PER = kGlrSlab / E, ROWS = 32 / PER;  // elements a copy, copies a row
+        const int c = lane % PER * E, r = lane / PER;
+        const bool in = c < left;
+#pragma unroll
+        for (int k = 0; k < TOK / ROWS; ++k) {
+            const int j = r + k * ROWS;
+            const bool ok = in && j < n;
+            cp_async<16>(to + j * kGlrSlab + c, ok ? from + j * ts + c : static_cast<const T*>(q.p), ok);
+        }
+    } else if (bytes) {
+        const int c = 2 * lane;
+#pragma unroll 4
+        for (int j = 0; j < TOK; ++j) {
+            const bool ok = c < left && j < n;
+            cp_async<2 * sizeof(T)>(to + j * kGlrSlab + c, ok ? from + j * ts + c : static_cast<const T*>(q.p), ok);
+        }
+    } else {
+        GlrRaw<T> v[TOK];
+        const int c = 2 * lane, nch = left - c > 1 ? 2 : (left - c > 0 ? 1 : 0);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) v[j] = glr_ld2<false>(from + j * ts + c, j < n ? nch : 0);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) *reinterpret_cast<GlrRaw<T>*>(to + j * kGlrSlab + c) = v[j];
+    }
+}
+// The lane's pair of row j.
+template <typename T>
+__device__ __forceinline__ float2 glr_row(const T* rows, int j) {
+    return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].get();
+}
+
+// Takes the block's first NS tiles; `slot` is shared memory.
+template <int NS>
+__device__ __forceinline__ void glr_first(const GlrSync& y, unsigned (&id)[NS], unsigned* slot) {
+    if (y.ticket) {
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int k = 0; k < NS; ++k) slot[k] = atomicAdd(y.ticket, 1u) + 1u;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < NS; ++k) id[k] = y.ticket ? slot[k] : blockIdx.x + k * gridDim.x;
+    __syncthreads();
+}
+
+// Stages of a block's copies: what two blocks on an SM leave room for.
+template <bool EPI>
+constexpr int kGlrFwdStages = EPI ? 1 : 2;
+template <typename T, bool EPI>
+constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + (EPI ? 2 : 0)) * kGlrTok<T> * kGlrSlab * (int)sizeof(T);
+
+template <typename T, bool VEC, bool EPI>
+__global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_fwd_kernel(const GlrParams p, const GlrSync y) {
+    constexpr int TOK = kGlrTok<T>, NS = kGlrFwdStages<EPI>, ROWS = TOK * kGlrSlab;
+    extern __shared__ __align__(16) unsigned char glr_smem[];
+    __shared__ float4 aggs[2][kGlrWarps][32];
+    __shared__ float2 enter[32];
+    __shared__ unsigned slot[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
+    T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrFwdWarpBytes<T, EPI>);
+    T* const epi = mine + 3 * NS * ROWS;
+    const int step = p.reverse ? -1 : 1;
+    const int tile_steps = nwarp * TOK;
+
+    auto copy_inputs = [&](unsigned id, int stage) {
+        if (id < y.total) {
+            const GlrTile t = glr_tile(p, id);
+            const int64_t ws = t.at * tile_steps + warp * TOK;
+            const int n = glr_steps(t.len, ws, TOK);
+            if (n) {
+                const int64_t t0 = p.reverse ? t.len - 1 - ws : ws;
+                T* to = mine + stage * 3 * ROWS;
+                glr_copy_rows<T, TOK>(to, p.r, t, t0, step, n, p.D, p.copy);
+                glr_copy_rows<T, TOK>(to + ROWS, p.i, t, t0, step, n, p.D, p.copy);
+                glr_copy_rows<T, TOK>(to + 2 * ROWS, p.x, t, t0, step, n, p.D, p.copy);
+            }
+        }
+        cp_async_commit();
+    };
+
+    unsigned ids[NS];
+    glr_first<NS>(y, ids, slot);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) copy_inputs(ids[k], k);
+    int stage = 0, par = 0;
+    while (ids[0] < y.total) {
+        const GlrTile t = glr_tile(p, ids[0]);
+        unsigned ahead = ids[NS - 1] + gridDim.x;
+        if (y.ticket && threadIdx.x == 0) ahead = atomicAdd(y.ticket, 1u) + 1u;
+        const int c0 = t.c + 2 * lane;
+        const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
+        const int64_t b = t.b, len = t.len, s0 = t.at * tile_steps, s1 = s0 + tile_steps;  // the tile's steps [s0, s1)
+        const int64_t ws = s0 + warp * TOK;
+        const int n = glr_steps(len, ws, TOK);
+        const int64_t t0 = p.reverse ? len - 1 - ws : ws;  // the token of the warp's first step
+        if (len < s1) glr_zero_rows<T, VEC>(p.out, b, len > s0 ? len : s0, s1 < p.L ? s1 : p.L, c0, nch, warp, nwarp);
+        if (len == 0 && s0 == 0 && warp == 0 && p.h_out)
+            glr_put2(p.h_out + b * p.D + c0, glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch), nch);
+        float4(*agg)[32] = aggs[par];
+        float2 Ps[TOK], hs[TOK];
+        cp_async_wait_pending<NS - 1>();
+        __syncwarp();
+        if constexpr (EPI) {
+            // every lane is past its last tile's phase 2
+            if (n && p.add.p) glr_copy_rows<T, TOK>(epi, p.add, t, t0, step, n, p.D, p.copy);
+            if (n && p.z.p) glr_copy_rows<T, TOK>(epi + ROWS, p.z, t, t0, step, n, p.D, p.copy);
+            cp_async_commit();
+        }
+        {
+            const T* in = mine + stage * 3 * ROWS;
+            const float2 A2 = glr_mul(glr_vec2(p.A + c0, nch), glr_f2(kGlrLog2e));
+            const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+            const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+            float2 P = glr_f2(1.f), h = glr_f2(0.f);
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
+                float2 a = g.a, w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in + 2 * ROWS, j));
+                if (j >= n) a = glr_f2(1.f), w = glr_f2(0.f);  // past the end: the state stays
+                P = glr_mul(P, a);
+                h = glr_fma(a, h, w);
+                Ps[j] = P;
+                hs[j] = h;
+            }
+            agg[warp][lane] = make_float4(P.x, h.x, P.y, h.y);
+        }
+        if (threadIdx.x == 0) slot[par] = ahead;
+        __syncthreads();
+        ahead = slot[par];
+        if (len > s0 && warp == 0) {
+            float2 P = glr_f2(1.f), h = glr_f2(0.f);
+            for (int w = 0; w < nwarp; ++w) {
+                const float4 q = agg[w][lane];
+                const float2 Pw = make_float2(q.x, q.z);
+                P = glr_mul(P, Pw);
+                h = glr_fma(Pw, h, make_float2(q.y, q.w));
+            }
+            const bool last = s1 >= len, publish = y.ticket && !last && !y.starve;
+            unsigned long long* map = y.map + (int64_t)t.rs * y.tiles * kGlrSlab + 2 * lane;
+            float* state = y.state + (int64_t)t.rs * y.groups * kGlrSlab + 2 * lane;
+            if (publish) glr_publish_map(map + t.at * kGlrSlab, P, h);
+            float2 c;
+            if (t.at == 0) {
+                // the other tiles take it from here, not from h_in, which may be h_out
+                c = glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch);
+                if (publish) glr_publish_state(state, c);
+            } else {
+                c = glr_lookback(y, map, state, t.at);
+            }
+            enter[lane] = c;
+            const float2 end = glr_fma(P, c, h);
+            if (publish && (t.at + 1) % kGlrGroup == 0) glr_publish_state(state + (t.at + 1) / kGlrGroup * kGlrSlab, end);
+            if (last && p.h_out) glr_put2(p.h_out + b * p.D + c0, end, nch);
+        }
+        copy_inputs(ahead, stage);
+        if (len > s0) {
+            __syncthreads();
+            float2 c = enter[lane];
+            for (int w = 0; w < warp; ++w) {
+                const float4 q = agg[w][lane];
+                c = glr_fma(make_float2(q.x, q.z), c, make_float2(q.y, q.w));
+            }
+            if (p.chunk && n > 0 && ws % kGlrChunk == 0)
+                glr_put2(p.chunk + (b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
+            if constexpr (EPI) {
+                cp_async_wait_pending<1>();  // all but the next tile's inputs
+                __syncwarp();
+            }
+            T* po = static_cast<T*>(p.out.p) + b * p.out.bs + t0 * p.out.ts + c0;
+            const int64_t ao = step * p.out.ts;
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                float2 h = glr_fma(Ps[j], c, hs[j]);
+                if constexpr (EPI) {
+                    if (p.add.p) h = glr_add(h, glr_row(epi, j));
+                    if (p.z.p) {
+                        const float2 z = glr_row(epi + ROWS, j);
+                        h = glr_mul(h, glr_mul(z, glr_sigmoid2(z)));
+                    }
+                }
+                glr_st2<VEC>(po + j * ao, h, j < n ? nch : 0);
+            }
+        }
+        par ^= 1;
+        if constexpr (NS == 2) {
+            ids[0] = ids[1];
+            stage ^= 1;
+        }
+        ids[NS - 1] = ahead;
+    }
+    cp_async_wait_all();
+}
+
+// Backward, tiles of kGlrChunk steps: they are walked from the last step to
+// the first (tile `at` from the end of the row's own tiles), and what they
+// hand over is q = a G, which the affine map of a tile takes from its right
+// end to its left.  A warp's steps share one product P for both scans, the
+// recomputed states (ascending, from the saved state that enters the tile)
+// and q (descending).  The second half reads x, dout, add and z again from
+// shared memory, so a warp's next copies start after it.
 constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
+template <typename T>
+constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
+template <typename T, bool EPI>
+constexpr int kGlrBwdWarpBytes = (EPI ? 6 : 4) * kGlrBwdStages<T> * kGlrBwdTok * kGlrSlab * (int)sizeof(T);
 
 template <typename T, bool VEC, bool EPI>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_bwd_kernel(const GlrParams p, const GlrSync y) {
-    constexpr int TOK = kGlrBwdTok;
+    constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI ? 6 : 4;
+    extern __shared__ __align__(16) unsigned char glr_smem[];
     __shared__ float2 aggP[kGlrWarps][32], aggh[kGlrWarps][32], aggq[kGlrWarps][32];
+    __shared__ float2 sums[3][kGlrWarps][32];
     __shared__ float2 enter[32];
-    __shared__ unsigned ticket;
+    __shared__ unsigned slot[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned id = blockIdx.x;
-    if (y.ticket) {
-        if (threadIdx.x == 0) ticket = atomicAdd(y.ticket, 1u) + 1u;
-        __syncthreads();
-        id = ticket;
-    }
-    const int slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
-    const unsigned chains = (unsigned)slabs * p.batch, rs = id % chains;
-    const int64_t tj = id / chains, b = rs / slabs;
-    const int c0 = (int)(rs % slabs) * kGlrSlab + 2 * lane;
-    const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
-    const int64_t len = glr_len(p, b), used = (len + kGlrChunk - 1) / kGlrChunk;  // the row's own tiles
-    const int64_t ti = tj < used ? used - 1 - tj : tj;
-    const int64_t s0 = ti * kGlrChunk, s1 = s0 + kGlrChunk;
-    float* part = p.part + ((int64_t)b * p.nchunk + ti) * 3 * p.D + c0;
-    if (len < s1) {
-        const int64_t z0 = len > s0 ? len : s0, z1 = s1 < p.L ? s1 : p.L;
-        glr_zero_rows<T, VEC>(p.dx, b, z0, z1, c0, nch, warp, kGlrWarps);
-        glr_zero_rows<T, VEC>(p.dr, b, z0, z1, c0, nch, warp, kGlrWarps);
-        glr_zero_rows<T, VEC>(p.di, b, z0, z1, c0, nch, warp, kGlrWarps);
-        if (EPI && p.add.p) glr_zero_rows<T, VEC>(p.dadd, b, z0, z1, c0, nch, warp, kGlrWarps);
-        if (EPI && p.z.p) glr_zero_rows<T, VEC>(p.dz, b, z0, z1, c0, nch, warp, kGlrWarps);
-    }
-    if (len <= s0) {
-        if (warp < 3) glr_put2(part + (int64_t)warp * p.D, glr_f2(0.f), nch);
-        if (tj == 0 && warp == 0 && p.dh_in)
-            glr_put2(p.dh_in + b * p.D + c0, glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch), nch);
-        return;
-    }
-
-    const int64_t ws = s0 + warp * TOK;
-    const int n = len - ws >= TOK ? TOK : (len > ws ? (int)(len - ws) : 0);
-    const int64_t t0 = p.reverse ? len - 1 - ws : ws;
+    T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrBwdWarpBytes<T, EPI>);
     const int step = p.reverse ? -1 : 1;
-    GlrRaw<T> rx[TOK], rd[TOK], ra[EPI ? TOK : 1], rz[EPI ? TOK : 1];
-    float2 rg[TOK], ig[TOK], a[TOK], hp[TOK];
-    const float2 A = glr_vec2(p.A + c0, nch);
-    {
-        GlrRaw<T> rr[TOK], ri[TOK];
-        const T* px = static_cast<const T*>(p.x.p) + b * p.x.bs + t0 * p.x.ts + c0;
-        const T* pr = static_cast<const T*>(p.r.p) + b * p.r.bs + t0 * p.r.ts + c0;
-        const T* pi = static_cast<const T*>(p.i.p) + b * p.i.bs + t0 * p.i.ts + c0;
-        const T* pd = static_cast<const T*>(p.dout.p) + b * p.dout.bs + t0 * p.dout.ts + c0;
-        const int64_t ax = step * p.x.ts, ar = step * p.r.ts, ai = step * p.i.ts, ad = step * p.dout.ts;
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const int m = j < n ? nch : 0;
-            rx[j] = glr_ld2<VEC>(px + j * ax, m);
-            rr[j] = glr_ld2<VEC>(pr + j * ar, m);
-            ri[j] = glr_ld2<VEC>(pi + j * ai, m);
-            rd[j] = glr_ld2<VEC>(pd + j * ad, m);
-            if constexpr (EPI) {
-                const int64_t t = t0 + step * j;
-                ra[j] = glr_ld2<VEC>(static_cast<const T*>(p.add.p) + b * p.add.bs + t * p.add.ts + c0, p.add.p ? m : 0);
-                rz[j] = glr_ld2<VEC>(static_cast<const T*>(p.z.p) + b * p.z.bs + t * p.z.ts + c0, p.z.p ? m : 0);
+    const float2 one = glr_f2(1.f), minus = glr_f2(-1.f);
+
+    // the tile's place along the row, in steps' order
+    auto index_of = [](const GlrTile& t) {
+        const int64_t used = (t.len + kGlrChunk - 1) / kGlrChunk;  // the row's own tiles
+        return t.at < used ? used - 1 - t.at : t.at;
+    };
+    auto copy_inputs = [&](unsigned id, int stage) {
+        if (id < y.total) {
+            const GlrTile t = glr_tile(p, id);
+            const int64_t ws = index_of(t) * kGlrChunk + warp * TOK;
+            const int n = glr_steps(t.len, ws, TOK);
+            if (n) {
+                const int64_t t0 = p.reverse ? t.len - 1 - ws : ws;
+                T* to = mine + stage * NT * ROWS;
+                glr_copy_rows<T, TOK>(to, p.r, t, t0, step, n, p.D, p.copy);
+                glr_copy_rows<T, TOK>(to + ROWS, p.i, t, t0, step, n, p.D, p.copy);
+                glr_copy_rows<T, TOK>(to + 2 * ROWS, p.x, t, t0, step, n, p.D, p.copy);
+                glr_copy_rows<T, TOK>(to + 3 * ROWS, p.dout, t, t0, step, n, p.D, p.copy);
+                if (EPI && p.add.p) glr_copy_rows<T, TOK>(to + 4 * ROWS, p.add, t, t0, step, n, p.D, p.copy);
+                if (EPI && p.z.p) glr_copy_rows<T, TOK>(to + 5 * ROWS, p.z, t, t0, step, n, p.D, p.copy);
             }
         }
-        const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-        const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-        float2 P = glr_f2(1.f), h = glr_f2(0.f);
+        cp_async_commit();
+    };
+
+    unsigned ids[NS];
+    glr_first<NS>(y, ids, slot);
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const GlrGate2 g = glr_gate2(rr[j].get(), ri[j].get(), nr, ni, A);
-            const float2 beta = make_float2(glr_sqrt(g.b2.x), glr_sqrt(g.b2.y));
-            float2 w = glr_mul(glr_mul(beta, g.ig), rx[j].get());
-            rg[j] = g.rg;
-            ig[j] = g.ig;
-            a[j] = g.a;
-            if (j >= n) a[j] = glr_f2(1.f), w = glr_f2(0.f);
-            hp[j] = h;  // the state before step j, from a zero state at the warp's first
-            P = glr_mul(P, a[j]);
-            h = glr_fma(a[j], h, w);
+    for (int k = 0; k < NS; ++k) copy_inputs(ids[k], k);
+    int stage = 0, par = 0;
+    while (ids[0] < y.total) {
+        const GlrTile t = glr_tile(p, ids[0]);
+        unsigned ahead = ids[NS - 1] + gridDim.x;
+        if (y.ticket && threadIdx.x == 0) ahead = atomicAdd(y.ticket, 1u) + 1u;
+        const int c0 = t.c + 2 * lane;
+        const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
+        const int64_t b = t.b, len = t.len, ti = index_of(t), s0 = ti * kGlrChunk, s1 = s0 + kGlrChunk;
+        const int64_t ws = s0 + warp * TOK;
+        const int n = glr_steps(len, ws, TOK);
+        const int64_t t0 = p.reverse ? len - 1 - ws : ws;
+        float* part = p.part + (b * p.nchunk + ti) * 3 * p.D + c0;
+        if (len < s1) {
+            const int64_t z0 = len > s0 ? len : s0, z1 = s1 < p.L ? s1 : p.L;
+            glr_zero_rows<T, VEC>(p.dx, b, z0, z1, c0, nch, warp, kGlrWarps);
+            glr_zero_rows<T, VEC>(p.dr, b, z0, z1, c0, nch, warp, kGlrWarps);
+            glr_zero_rows<T, VEC>(p.di, b, z0, z1, c0, nch, warp, kGlrWarps);
+            if (EPI && p.add.p) glr_zero_rows<T, VEC>(p.dadd, b, z0, z1, c0, nch, warp, kGlrWarps);
+            if (EPI && p.z.p) glr_zero_rows<T, VEC>(p.dz, b, z0, z1, c0, nch, warp, kGlrWarps);
         }
-        float2 q = glr_f2(0.f);
+        const bool active = len > s0;
+        if (!active) {
+            if (warp < 3) glr_put2(part + (int64_t)warp * p.D, glr_f2(0.f), nch);
+            if (t.at == 0 && warp == 0 && p.dh_in)
+                glr_put2(p.dh_in + b * p.D + c0, glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch), nch);
+        }
+        const T* in = mine + stage * NT * ROWS;
+        const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_add = in + 4 * ROWS, *in_z = in + 5 * ROWS;
+        float2 rg[TOK], ig[TOK], u[TOK], hp[TOK];
+        const float2 A = glr_vec2(p.A + c0, nch);
+        float2 entering = glr_f2(0.f);
+        if (active) entering = glr_vec2(p.chunk + (b * p.nchunk + ti) * p.D + c0, nch);
+        cp_async_wait_pending<NS - 1>();
+        __syncwarp();
+        {
+            const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+            const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+            const float2 A2 = glr_mul(A, glr_f2(kGlrLog2e));
+            float2 P = one, h = glr_f2(0.f);
 #pragma unroll
-        for (int j = TOK - 1; j >= 0; --j) {
-            float2 dh = rd[j].get();
-            if constexpr (EPI) {
-                if (p.z.p) dh = glr_mul(dh, glr_mul(rz[j].get(), glr_sigmoid2(rz[j].get())));
+            for (int j = 0; j < TOK; ++j) {
+                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
+                float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in_x, j)), a = g.a;
+                rg[j] = g.rg;
+                ig[j] = make_float2(glr_rcp(g.di.x), glr_rcp(g.di.y));
+                u[j] = g.u;
+                if (j >= n) a = one, u[j] = w = glr_f2(0.f);
+                hp[j] = h;  // the state before step j, from a zero state at the warp's first
+                P = glr_mul(P, a);
+                h = glr_fma(a, h, w);
             }
-            q = glr_mul(a[j], glr_add(q, dh));  // past the end dout reads as 0 and a is 1
-        }
-        aggP[warp][lane] = P;
-        aggh[warp][lane] = h;
-        aggq[warp][lane] = q;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float2 P = glr_f2(1.f), q = glr_f2(0.f);
-        for (int w = kGlrWarps - 1; w >= 0; --w) {
-            P = glr_mul(P, aggP[w][lane]);
-            q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
-        }
-        const bool last = ti == 0, publish = y.ticket && !last && !y.starve;
-        unsigned long long* map = y.map + (int64_t)rs * y.tiles * kGlrSlab + 2 * lane;
-        float* state = y.state + (int64_t)rs * y.groups * kGlrSlab + 2 * lane;
-        if (publish) glr_publish_map(map + tj * kGlrSlab, P, q);
-        float2 c;
-        if (tj == 0) {
-            c = glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch);
-            if (publish) glr_publish_state(state, c);
-        } else {
-            c = glr_lookback(y, map, state, tj);
-        }
-        enter[lane] = c;
-        const float2 end = glr_fma(P, c, q);
-        if (publish && (tj + 1) % kGlrGroup == 0) glr_publish_state(state + (tj + 1) / kGlrGroup * kGlrSlab, end);
-        if (last && p.dh_in) glr_put2(p.dh_in + b * p.D + c0, end, nch);
-    }
-    {
-        // the states before the warp's steps, from the one that enters the tile
-        float2 c = glr_vec2(p.chunk + (b * p.nchunk + ti) * p.D + c0, nch);
-        for (int w = 0; w < warp; ++w) c = glr_fma(aggP[w][lane], c, aggh[w][lane]);
-        float2 P = c;
+            float2 q = glr_f2(0.f);
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            hp[j] = glr_add(P, hp[j]);
-            P = glr_mul(P, a[j]);
-        }
-    }
-    __syncthreads();
-    float2 q = enter[lane];
-    for (int w = kGlrWarps - 1; w > warp; --w) q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
-    __syncthreads();  // the maps are read: their place takes the sums below
-    float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
-    const float2 one = glr_f2(1.f);
-#pragma unroll
-    for (int j = TOK - 1; j >= 0; --j) {
-        const int m = j < n ? nch : 0;
-        const int64_t t = t0 + step * j;
-        const float2 la = glr_mul(A, rg[j]), t2 = glr_add(la, la);
-        const float2 b2 = make_float2(glr_one_minus_a2(t2.x, a[j].x), glr_one_minus_a2(t2.y, a[j].y));
-        const float2 rs2 = make_float2(glr_rsqrt(b2.x), glr_rsqrt(b2.y));
-        const float2 bi = glr_mul(glr_mul(b2, rs2), ig[j]), w = glr_mul(bi, rx[j].get());
-        float2 dh = rd[j].get();
-        if constexpr (EPI) {
-            if (p.z.p) {
-                const float2 z = rz[j].get(), sz = glr_sigmoid2(z);
-                const float2 h = glr_add(glr_fma(a[j], hp[j], w), ra[j].get());
-                // silu'(z) = s (1 + z (1 - s))
-                const float2 ds = glr_mul(sz, glr_fma(z, glr_fma(sz, glr_f2(-1.f), one), one));
-                glr_st2<VEC>(static_cast<T*>(p.dz.p) + b * p.dz.bs + t * p.dz.ts + c0, glr_mul(glr_mul(dh, h), ds), m);
-                dh = glr_mul(dh, glr_mul(z, sz));
+            for (int j = TOK - 1; j >= 0; --j) {
+                float2 dh = glr_row(in_d, j);
+                if constexpr (EPI) {
+                    if (p.z.p) {
+                        const float2 z = glr_row(in_z, j);
+                        dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
+                    }
+                }
+                if (j >= n) dh = glr_f2(0.f);
+                const float2 G = glr_add(q, dh);
+                q = glr_fma(u[j], glr_mul(G, minus), G);  // a G; past the end u is 0
             }
-            if (p.add.p) glr_st2<VEC>(static_cast<T*>(p.dadd.p) + b * p.dadd.bs + t * p.dadd.ts + c0, dh, m);
+            aggP[warp][lane] = P;
+            aggh[warp][lane] = h;
+            aggq[warp][lane] = q;
         }
-        const float2 G = glr_add(dh, q);
-        q = glr_mul(a[j], G);
-        // (a / beta)^2 w, with beta = 0 giving 0 (its 1/beta below is then 0 too)
-        const float2 ar = glr_mul(a[j], rs2);
-        const float2 dla = glr_mul(G, glr_fma(a[j], hp[j], glr_mul(glr_mul(ar, ar), glr_mul(w, glr_f2(-1.f)))));
-        const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_fma(rg[j], glr_f2(-1.f), one)));
-        const float2 di = glr_mul(glr_mul(G, w), glr_fma(ig[j], glr_f2(-1.f), one));
-        glr_st2<VEC>(static_cast<T*>(p.dx.p) + b * p.dx.bs + t * p.dx.ts + c0, glr_mul(G, bi), m);
-        glr_st2<VEC>(static_cast<T*>(p.dr.p) + b * p.dr.bs + t * p.dr.ts + c0, dr, m);
-        glr_st2<VEC>(static_cast<T*>(p.di.p) + b * p.di.bs + t * p.di.ts + c0, di, m);
-        if (j < n) {
-            sA = glr_fma(rg[j], dla, sA);
-            sr = glr_add(sr, dr);
-            si = glr_add(si, di);
+        if (threadIdx.x == 0) slot[par] = ahead;
+        __syncthreads();
+        ahead = slot[par];
+        if (active) {
+            if (warp == 0) {
+                float2 P = one, q = glr_f2(0.f);
+                for (int w = kGlrWarps - 1; w >= 0; --w) {
+                    P = glr_mul(P, aggP[w][lane]);
+                    q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
+                }
+                const bool last = ti == 0, publish = y.ticket && !last && !y.starve;
+                unsigned long long* map = y.map + (int64_t)t.rs * y.tiles * kGlrSlab + 2 * lane;
+                float* state = y.state + (int64_t)t.rs * y.groups * kGlrSlab + 2 * lane;
+                if (publish) glr_publish_map(map + t.at * kGlrSlab, P, q);
+                float2 c;
+                if (t.at == 0) {
+                    c = glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch);
+                    if (publish) glr_publish_state(state, c);
+                } else {
+                    c = glr_lookback(y, map, state, t.at);
+                }
+                enter[lane] = c;
+                const float2 end = glr_fma(P, c, q);
+                if (publish && (t.at + 1) % kGlrGroup == 0)
+                    glr_publish_state(state + (t.at + 1) / kGlrGroup * kGlrSlab, end);
+                if (last && p.dh_in) glr_put2(p.dh_in + b * p.D + c0, end, nch);
+            }
+            {
+                // the states before the warp's steps, from the one that enters the tile
+                float2 c = entering;
+                for (int w = 0; w < warp; ++w) c = glr_fma(aggP[w][lane], c, aggh[w][lane]);
+#pragma unroll
+                for (int j = 0; j < TOK; ++j) {
+                    hp[j] = glr_add(c, hp[j]);
+                    c = glr_fma(u[j], glr_mul(c, minus), c);
+                }
+            }
+            __syncthreads();
+            float2 q = enter[lane];
+            for (int w = kGlrWarps - 1; w > warp; --w) q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
+            float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
+#pragma unroll
+            for (int j = TOK - 1; j >= 0; --j) {
+                const int m = j < n ? nch : 0;
+                const int64_t tk = t0 + step * j;
+                const float2 a = glr_fma(u[j], minus, one), b2 = glr_mul(u[j], glr_add(a, one));
+                const float2 b2t = glr_add(b2, glr_f2(kGlrTiny));
+                const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
+                const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
+                float2 dh = glr_row(in_d, j);
+                if constexpr (EPI) {
+                    if (p.z.p) {
+                        const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
+                        float2 h = glr_fma(a, hp[j], w);
+                        if (p.add.p) h = glr_add(h, glr_row(in_add, j));
+                        // silu'(z) = s (1 + z (1 - s))
+                        const float2 ds = glr_mul(sz, glr_fma(z, glr_fma(sz, minus, one), one));
+                        glr_st2<VEC>(static_cast<T*>(p.dz.p) + b * p.dz.bs + tk * p.dz.ts + c0,
+                                     glr_mul(glr_mul(dh, h), ds), m);
+                        dh = glr_mul(dh, glr_mul(z, sz));
+                    }
+                    if (p.add.p) glr_st2<VEC>(static_cast<T*>(p.dadd.p) + b * p.dadd.bs + tk * p.dadd.ts + c0, dh, m);
+                }
+                if (j >= n) continue;
+                const float2 G = glr_add(dh, q);
+                q = glr_mul(a, G);
+                const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
+                const float2 dla = glr_mul(G, glr_fma(a, hp[j], glr_mul(glr_mul(ab, ab), glr_mul(w, minus))));
+                const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_fma(rg[j], minus, one)));
+                const float2 di = glr_mul(glr_mul(G, w), glr_fma(ig[j], minus, one));
+                glr_st2<VEC>(static_cast<T*>(p.dx.p) + b * p.dx.bs + tk * p.dx.ts + c0, glr_mul(G, bi), m);
+                glr_st2<VEC>(static_cast<T*>(p.dr.p) + b * p.dr.bs + tk * p.dr.ts + c0, dr, m);
+                glr_st2<VEC>(static_cast<T*>(p.di.p) + b * p.di.bs + tk * p.di.ts + c0, di, m);
+                sA = glr_fma(rg[j], dla, sA);
+                sr = glr_add(sr, dr);
+                si = glr_add(si, di);
+            }
+            sums[0][warp][lane] = sA;
+            sums[1][warp][lane] = sr;
+            sums[2][warp][lane] = si;
         }
+        __syncwarp();  // every lane has read its rows
+        copy_inputs(ahead, stage);
+        if (active) {
+            __syncthreads();
+            if (warp < 3) {
+                float2 v = glr_f2(0.f);
+                for (int w = 0; w < kGlrWarps; ++w) v = glr_add(v, sums[warp][w][lane]);
+                glr_put2(part + (int64_t)warp * p.D, v, nch);
+            }
+        }
+        par ^= 1;
+        if constexpr (NS == 2) {
+            ids[0] = ids[1];
+            stage ^= 1;
+        }
+        ids[NS - 1] = ahead;
     }
-    aggP[warp][lane] = sA;
-    aggh[warp][lane] = sr;
-    aggq[warp][lane] = si;
-    __syncthreads();
-    if (warp < 3) {
-        const float2(*from)[32] = warp == 0 ? aggP : (warp == 1 ? aggh : aggq);
-        float2 v = glr_f2(0.f);
-        for (int w = 0; w < kGlrWarps; ++w) v = glr_add(v, from[w][lane]);
-        glr_put2(part + (int64_t)warp * p.D, v, nch);
-    }
+    cp_async_wait_all();
 }
 
 // The three sums over the partial rows [n][3][D]: a block takes 32 columns, each

@@ -2,6 +2,8 @@
 // argument checks, launch shapes and dispatch.  The arithmetic is in glr.cuh.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "api_util.h"
 #include "bimamba.h"
 #include "glr.cuh"
@@ -126,9 +128,35 @@ int make_sync(bimamba::GlrSync& y, int batch, int D, int64_t tiles, unsigned fla
     return cudaMemsetAsync(ws, 0xff, sync_bytes(batch, D, tiles), st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
 }
 
-// Pairs of channels in one access: every row of q starts at an even element of a pair-aligned pointer.
-bool paired(const GlrRows& q, size_t esz) {
-    return !q.p || (aligned(q.p, 2 * esz) && q.bs % 2 == 0 && q.ts % 2 == 0);
+// Rows whose every start is aligned to `n` elements.
+bool starts_at(const GlrRows& q, size_t esz, int n) {
+    return !q.p || (aligned(q.p, n * esz) && q.bs % n == 0 && q.ts % n == 0);
+}
+
+// Bytes of one asynchronous copy that all rows read allow: 16, a pair, or 0 (single elements).
+template <typename... R>
+int copy_bytes(int D, size_t esz, R... q) {
+    const int wide = (int)(16 / esz);
+    if (D % wide == 0 && (starts_at(q, esz, wide) && ...)) return 16;
+    return D % 2 == 0 && (starts_at(q, esz, 2) && ...) ? (int)(2 * esz) : 0;
+}
+
+// Blocks that stay: what the SMs hold at 128 registers a thread.
+int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, int64_t tiles, int warps,
+                 size_t warp_bytes, unsigned flags, void* ws, cudaStream_t st) {
+    const int64_t total = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    // tickets run past the total by what the blocks take ahead
+    if (total > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
+    bimamba::GlrSync y;
+    int rc = make_sync(y, k.batch, k.D, tiles, flags, ws, st);
+    if (rc) return rc;
+    y.total = (unsigned)total;
+    const size_t smem = warps * warp_bytes;
+    if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), bimamba::kGlrWarps * warp_bytes))) return rc;
+    const int by_regs = 16 / warps, by_smem = (int)(227 * 1024 / (smem + 12 * 1024));
+    const int64_t held = (int64_t)kSms * std::max(1, std::min(by_regs, by_smem));
+    fn<<<(unsigned)std::min(total, held), warps * 32, smem, st>>>(k, y);
+    return launch_status();
 }
 
 template <typename T, bool VEC>
@@ -136,30 +164,20 @@ int launch_fwd(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
     const int64_t tiles = (k.L + TILE - 1) / TILE;
     const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
-    const int64_t blocks = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
-    if (blocks > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
-    bimamba::GlrSync y;
-    int rc = make_sync(y, k.batch, k.D, tiles, flags, ws, st);
-    if (rc) return rc;
     if (k.add.p || k.z.p)
-        bimamba::glr_tile_fwd_kernel<T, VEC, true><<<(unsigned)blocks, warps * 32, 0, st>>>(k, y);
-    else
-        bimamba::glr_tile_fwd_kernel<T, VEC, false><<<(unsigned)blocks, warps * 32, 0, st>>>(k, y);
-    return launch_status();
+        return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, true>, k, tiles, warps,
+                            bimamba::kGlrFwdWarpBytes<T, true>, flags, ws, st);
+    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, false>, k, tiles, warps,
+                        bimamba::kGlrFwdWarpBytes<T, false>, flags, ws, st);
 }
 
 template <typename T, bool VEC>
 int launch_bwd(const GlrParams& k, unsigned flags, void* sync, cudaStream_t st) {
-    const int64_t blocks = k.nchunk * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
-    if (blocks > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
-    bimamba::GlrSync y;
-    int rc = make_sync(y, k.batch, k.D, k.nchunk, flags, sync, st);
-    if (rc) return rc;
     if (k.add.p || k.z.p)
-        bimamba::glr_tile_bwd_kernel<T, VEC, true><<<(unsigned)blocks, bimamba::kGlrWarps * 32, 0, st>>>(k, y);
-    else
-        bimamba::glr_tile_bwd_kernel<T, VEC, false><<<(unsigned)blocks, bimamba::kGlrWarps * 32, 0, st>>>(k, y);
-    return launch_status();
+        return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, true>, k, k.nchunk, bimamba::kGlrWarps,
+                            bimamba::kGlrBwdWarpBytes<T, true>, flags, sync, st);
+    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, false>, k, k.nchunk, bimamba::kGlrWarps,
+                        bimamba::kGlrBwdWarpBytes<T, false>, flags, sync, st);
 }
 
 // The backward's partial sums, one row of 3 D per chunk, in whole 256 bytes.
@@ -196,8 +214,8 @@ int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     k.chunk = chunk_states;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const size_t e = elem_size(in->dtype);
-    const bool vec = d_inner % 2 == 0 && paired(k.x, e) && paired(k.r, e) && paired(k.i, e) && paired(k.add, e) &&
-                     paired(k.z, e) && paired(k.out, e);
+    k.copy = copy_bytes(d_inner, e, k.x, k.r, k.i, k.add, k.z);
+    const bool vec = d_inner % 2 == 0 && starts_at(k.out, e, 2);
     if (in->dtype == BIMAMBA_BF16)
         return vec ? launch_fwd<bf16, true>(k, flags, workspace, st) : launch_fwd<bf16, false>(k, flags, workspace, st);
     return vec ? launch_fwd<float, true>(k, flags, workspace, st) : launch_fwd<float, false>(k, flags, workspace, st);
@@ -236,9 +254,9 @@ int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     k.part = static_cast<float*>(workspace);
     unsigned char* sync = static_cast<unsigned char*>(workspace) + part_bytes(batch, L, d_inner);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    const bool vec = d_inner % 2 == 0 && paired(k.x, e) && paired(k.r, e) && paired(k.i, e) && paired(k.add, e) &&
-                     paired(k.z, e) && paired(k.dout, e) && paired(k.dx, e) && paired(k.dr, e) && paired(k.di, e) &&
-                     (!k.add.p || paired(k.dadd, e)) && (!k.z.p || paired(k.dz, e));
+    k.copy = copy_bytes(d_inner, e, k.x, k.r, k.i, k.dout, k.add, k.z);
+    const bool vec = d_inner % 2 == 0 && starts_at(k.dx, e, 2) && starts_at(k.dr, e, 2) && starts_at(k.di, e, 2) &&
+                     (!k.add.p || starts_at(k.dadd, e, 2)) && (!k.z.p || starts_at(k.dz, e, 2));
     if (in->dtype == BIMAMBA_BF16)
         rc = vec ? launch_bwd<bf16, true>(k, flags, sync, st) : launch_bwd<bf16, false>(k, flags, sync, st);
     else

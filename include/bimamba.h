@@ -453,7 +453,7 @@ typedef struct {
 
 /* Parameters of the direction, fp32 device pointers. */
 typedef struct {
-    const float *A;       /* [d_inner], <= 0: the log decay of a wide-open gate (a positive entry gives NaN) */
+    const float *A;       /* [d_inner], <= 0: the log decay of a wide-open gate (a positive entry is undefined) */
     const float *r_bias;  /* [d_inner] or NULL (= 0) */
     const float *i_bias;  /* [d_inner] or NULL (= 0) */
 } bimamba_glr_params_t;
