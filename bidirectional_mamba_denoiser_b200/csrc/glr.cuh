@@ -21,6 +21,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tma_util.cuh"
 
 namespace bimamba {
@@ -28,15 +30,17 @@ namespace bimamba {
 constexpr int kGlrChunk = 64;
 constexpr float kGlrLog2e = 1.4426950408889634f;
 
-// Rows of one tensor: element (b, t, d) at p[b * bs + t * ts + d].
+// Rows of one tensor: the element of channel 0 of (b, t) is at p + b * bs +
+// t * |ts| bytes, and the next step's ts bytes on (ts < 0 in reverse).
 struct GlrRows {
-    void* p;
-    int64_t bs, ts;
+    char* p;
+    int64_t bs;
+    int ts;
 };
+enum { kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ, kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors };
 
 struct GlrParams {
-    GlrRows x, r, i, add, z, out;          // add.p, z.p may be null
-    GlrRows dout, dx, dr, di, dadd, dz;    // backward
+    GlrRows rows[kGlrTensors];  // p null where the call has none
     const float* A;
     const float* r_bias;   // or null
     const float* i_bias;   // or null
@@ -95,6 +99,9 @@ __device__ __forceinline__ float2 glr_f2(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 glr_mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 glr_add(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 glr_fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 glr_fma(float2 a, float2 b, float c) { return glr_fma(a, b, glr_f2(c)); }
+__device__ __forceinline__ float2 glr_add(float2 a, float b) { return glr_add(a, glr_f2(b)); }
+__device__ __forceinline__ float2 glr_sub(float2 a, float2 b) { return glr_fma(b, glr_f2(-1.f), a); }
 
 // Two channels as they lie in memory: packed for bf16, so that a tile's
 // loads in flight cost one register a pair.
@@ -113,33 +120,8 @@ struct GlrRaw<float> {
     __device__ __forceinline__ float2 get() const { return v; }
 };
 
-// VEC: one access for the pair (channel count and strides even, pointers
-// aligned to the pair); else one per channel, `n` (0..2) of them in range.
-template <bool VEC>
-__device__ __forceinline__ GlrRaw<__nv_bfloat16> glr_ld2(const __nv_bfloat16* p, int n) {
-    GlrRaw<__nv_bfloat16> r;
-    r.v = 0u;
-    if constexpr (VEC) {
-        if (n) r.v = __ldcs(reinterpret_cast<const unsigned int*>(p));
-    } else {
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-        if (n > 0) r.v = q[0];
-        if (n > 1) r.v |= (uint32_t)q[1] << 16;
-    }
-    return r;
-}
-template <bool VEC>
-__device__ __forceinline__ GlrRaw<float> glr_ld2(const float* p, int n) {
-    GlrRaw<float> r;
-    r.v = make_float2(0.f, 0.f);
-    if constexpr (VEC) {
-        if (n) r.v = __ldcs(reinterpret_cast<const float2*>(p));
-    } else {
-        if (n > 0) r.v.x = p[0];
-        if (n > 1) r.v.y = p[1];
-    }
-    return r;
-}
+// Stores of n (0..2) channels of a pair.  VEC: one access (channel count and
+// strides even, pointers aligned to the pair, so n is 0 or 2).
 template <bool VEC>
 __device__ __forceinline__ void glr_st2(__nv_bfloat16* p, float2 v, int n) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);  // to nearest even
@@ -159,13 +141,12 @@ __device__ __forceinline__ void glr_st2(float* p, float2 v, int n) {
         if (n > 1) p[1] = v.y;
     }
 }
-// fp32 vectors (parameters, states): always element by element, `n` of them.
-__device__ __forceinline__ float2 glr_vec2(const float* p, int n) {
-    return make_float2(p && n > 0 ? p[0] : 0.f, p && n > 1 ? p[1] : 0.f);
-}
-__device__ __forceinline__ void glr_put2(float* p, float2 v, int n) {
-    if (n > 0) p[0] = v.x;
-    if (n > 1) p[1] = v.y;
+// A pair of an fp32 vector, zeros where it is null.
+template <bool VEC>
+__device__ __forceinline__ float2 glr_vec2(const float* p, int64_t c, int n) {
+    if (!p || n == 0) return make_float2(0.f, 0.f);
+    if constexpr (VEC) return *reinterpret_cast<const float2*>(p + c);
+    return make_float2(p[c], n > 1 ? p[c + 1] : 0.f);
 }
 
 __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(glr_sigmoid(v.x), glr_sigmoid(v.y)); }
@@ -179,18 +160,22 @@ __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(gl
 __device__ __forceinline__ float2 glr_one_minus_ex2(float2 l) {
     constexpr float kMagic = 12582912.f;
     l = make_float2(glr_max_nan(l.x, -126.f), glr_max_nan(l.y, -126.f));
-    const float2 m = glr_add(l, glr_f2(kMagic));
-    const float2 f = glr_fma(glr_add(m, glr_f2(-kMagic)), glr_f2(-1.f), l);
-    float2 q = glr_fma(f, glr_f2(0.00015403512225020677f), glr_f2(0.0013390735257416964f));
-    q = glr_fma(f, q, glr_f2(0.009618237614631653f));
-    q = glr_fma(f, q, glr_f2(0.05550357326865196f));
-    q = glr_fma(f, q, glr_f2(0.24022649228572845f));
-    q = glr_fma(f, q, glr_f2(0.6931471824645996f));
+    const float2 m = glr_add(l, kMagic);
+    const float2 f = glr_sub(l, glr_add(m, -kMagic));
+    float2 q = glr_fma(f, glr_f2(0.00015403512225020677f), 0.0013390735257416964f);
+    q = glr_fma(f, q, 0.009618237614631653f);
+    q = glr_fma(f, q, 0.05550357326865196f);
+    q = glr_fma(f, q, 0.24022649228572845f);
+    q = glr_fma(f, q, 0.6931471824645996f);
     q = glr_mul(f, q);
     // -2^n, its exponent from the low bits of m
     const float2 s = make_float2(__uint_as_float((__float_as_uint(m.x) << 23) + 0xbf800000u),
                                  __uint_as_float((__float_as_uint(m.y) << 23) + 0xbf800000u));
-    return glr_fma(q, s, glr_add(s, glr_f2(1.f)));
+    return glr_fma(q, s, glr_add(s, 1.f));
+}
+
+__device__ __forceinline__ float2 glr_one_minus(float2 v) {
+    return glr_fma(v, glr_f2(-1.f), glr_f2(1.f));
 }
 
 // The gates of a pair: r, i raw activations; nr, ni: -bias log2 e; A2: A log2 e.
@@ -200,12 +185,12 @@ struct GlrGate2 {
 __device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 A2) {
     GlrGate2 g;
     const float2 er = glr_fma(r, glr_f2(-kGlrLog2e), nr), ei = glr_fma(i, glr_f2(-kGlrLog2e), ni);
-    const float2 dr = glr_add(make_float2(glr_ex2(er.x), glr_ex2(er.y)), glr_f2(1.f));
-    g.di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), glr_f2(1.f));
+    const float2 dr = glr_add(make_float2(glr_ex2(er.x), glr_ex2(er.y)), 1.f);
+    g.di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), 1.f);
     g.rg = make_float2(glr_rcp(dr.x), glr_rcp(dr.y));
     g.u = glr_one_minus_ex2(glr_mul(A2, g.rg));
-    g.a = glr_fma(g.u, glr_f2(-1.f), glr_f2(1.f));
-    g.b2 = glr_mul(g.u, glr_add(g.a, glr_f2(1.f)));
+    g.a = glr_one_minus(g.u);
+    g.b2 = glr_mul(g.u, glr_add(g.a, 1.f));
     return g;
 }
 // The smallest normal, added under every 1 / beta: 0 / 0 becomes 0, and down to
@@ -214,7 +199,7 @@ constexpr float kGlrTiny = 1.17549435e-38f;
 // beta ig with one special function: b2 / sqrt(b2 di^2) = sqrt(b2) / di (where
 // di^2 overflows, an input gate below e^-44, it counts as closed).
 __device__ __forceinline__ float2 glr_beta_ig(float2 b2, float2 di) {
-    const float2 v = glr_mul(glr_mul(glr_add(b2, glr_f2(kGlrTiny)), di), di);
+    const float2 v = glr_mul(glr_mul(glr_add(b2, kGlrTiny), di), di);
     return glr_mul(b2, make_float2(glr_rsqrt(v.x), glr_rsqrt(v.y)));
 }
 
@@ -232,12 +217,14 @@ __device__ __forceinline__ float2 glr_beta_ig(float2 b2, float2 di) {
 // publishes the state that enters the next group.  A tile reads that state
 // and the maps of its group's earlier tiles and applies them in order, so the
 // result is bit for bit that of the plain chain whatever the timing, while
-// only one hop in kGlrGroup waits on another tile's wait.  A published pair is one
-// 64-bit word (or a float each), written once over an all-ones fill that no
-// result has (a NaN of that pattern is replaced), so it needs no flag and no
-// fence.  Tiles are taken in ticket order and a block works through its own in
-// that order, so whatever a tile waits for is being worked on; every wait is
-// bounded, and once one has run out the launch's other waits end as well.
+// only one hop in kGlrGroup waits on another tile's wait.  Each warp fetches one
+// of the eight pieces, asked for before its steps and looked at after them, so
+// what is there already costs no latency.  A published pair is one 64-bit word
+// (or a float each), written once over an all-ones fill that no result has (a
+// NaN of that pattern is replaced), so it needs no flag and no fence.  Tiles
+// are taken in ticket order and a block works through its own in that order,
+// so whatever a tile waits for is being worked on; every wait is bounded, and
+// once one has run out the launch's other waits end as well.
 //
 // Blocks stay (as many as the GPU holds) and take the next tile's ticket while
 // they work on one.  Each warp copies the rows of its own steps into its own
@@ -246,6 +233,7 @@ __device__ __forceinline__ float2 glr_beta_ig(float2 b2, float2 di) {
 // copies only.
 constexpr int kGlrSlab = 64;
 constexpr int kGlrGroup = 8;
+static_assert(kGlrGroup == 8, "a piece for each warp");
 constexpr unsigned kGlrErrTimeout = 4u;  // a wait for an earlier tile gave up
 
 static __device__ unsigned int g_glr_error;
@@ -275,83 +263,145 @@ __device__ __forceinline__ void glr_publish_state(float* q, float2 h) {
                  : "memory");
 }
 
-// The state entering tile `ti`: the group's entering state carried through
-// the group's earlier maps.  map, state: of this row and slab, at the lane's
-// pair.  Each lane waits for its own two channels.
-__device__ __forceinline__ float2 glr_lookback(const GlrSync& y, const unsigned long long* map, const float* state,
-                                               int64_t ti) {
-    const int64_t g = ti / kGlrGroup, first = g * kGlrGroup;
-    const int n = (int)(ti - first);
-    unsigned long long m[kGlrGroup - 1][2];
-    unsigned s0, s1;
-    const long long t0 = clock64();
-    bool ready = false;
-    while (!ready) {
-        asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];"
-                     : "=r"(s0), "=r"(s1)
-                     : "l"(state + g * kGlrSlab)
-                     : "memory");
-        ready = s0 != 0xffffffffu && s1 != 0xffffffffu;
-#pragma unroll
-        for (int k = 0; k < kGlrGroup - 1; ++k) {
-            if (k >= n) continue;
-            asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
-                         : "=l"(m[k][0]), "=l"(m[k][1])
-                         : "l"(map + (first + k) * kGlrSlab)
-                         : "memory");
-            // P lies in [0, 1] (or is NaN, 0x7fffffff): never the fill
-            ready = ready && (unsigned)m[k][0] != 0xffffffffu && (unsigned)m[k][1] != 0xffffffffu;
-        }
-        if (ready) break;
-        unsigned gone;
-        asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(gone) : "l"(y.ticket + 1) : "memory");
-        if (gone == 0u || clock64() - t0 > y.wait_limit) {
-            atomicExch(y.ticket + 1, 0u);
-            atomicOr(&g_glr_error, kGlrErrTimeout);
-            break;
-        }
-    }
-    __syncwarp();
-    float2 c = ready ? make_float2(__uint_as_float(s0), __uint_as_float(s1)) : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kGlrGroup - 1; ++k) {
-        if (k >= n || !ready) continue;
-        const float2 P = make_float2(__uint_as_float((unsigned)m[k][0]), __uint_as_float((unsigned)m[k][1]));
-        const float2 h = make_float2(__uint_as_float((unsigned)(m[k][0] >> 32)), __uint_as_float((unsigned)(m[k][1] >> 32)));
-        c = glr_fma(P, c, h);
-    }
-    return c;
-}
-
 // Steps a warp scans: what its registers hold with two blocks of 256 threads on an SM.
 template <typename T>
 constexpr int kGlrTok = sizeof(T) == 2 ? 16 : 8;
 constexpr int kGlrWarps = 8;
 
-// The rest of a row behind its length: zeros from token t0 up to t1.
-template <typename T, bool VEC>
-__device__ __forceinline__ void glr_zero_rows(const GlrRows& q, int64_t b, int64_t t0, int64_t t1, int c0, int nch,
-                                              int warp, int nwarp) {
-    for (int64_t t = t0 + warp; t < t1; t += nwarp)
-        glr_st2<VEC>(static_cast<T*>(q.p) + b * q.bs + t * q.ts + c0, make_float2(0.f, 0.f), nch);
+// Where a tile lies: `at` counts tiles along the row in the order in which
+// they are walked (below 0: there is none), rs is row * slabs + slab.
+struct GlrTile {
+    int at, rs, b, len;
+};
+__device__ __forceinline__ int glr_slabs(const GlrParams& p) { return (p.D + kGlrSlab - 1) / kGlrSlab; }
+__device__ __forceinline__ GlrTile glr_tile(const GlrParams& p, const GlrSync& y, unsigned id) {
+    if (id >= y.total) return {-1, 0, 0, 0};
+    const unsigned slabs = glr_slabs(p), chains = slabs * (unsigned)p.batch;
+    GlrTile t;
+    t.at = (int)(id / chains);
+    t.rs = (int)(id % chains);
+    t.b = t.rs / (int)slabs;
+    t.len = (int)glr_len(p, t.b);
+    return t;
+}
+__device__ __forceinline__ int glr_channel(const GlrParams& p, const GlrTile& t) {
+    return (t.rs - t.b * glr_slabs(p)) * kGlrSlab;
+}
+// What a warp fetches for a tile that is not its row's first: warp w < 7 the
+// map of the group's tile w, warp 7 the state that enters the group.
+struct GlrPiece {
+    unsigned long long v[2];
+};
+// The lane's place in the map of the row's tile `at`, and in the state that enters its group.
+__device__ __forceinline__ unsigned long long* glr_map(const GlrSync& y, const GlrTile& t, int at) {
+    return y.map + (t.rs * y.tiles + at) * kGlrSlab + 2 * (threadIdx.x & 31);
+}
+__device__ __forceinline__ float* glr_state(const GlrSync& y, const GlrTile& t, int at) {
+    return y.state + (t.rs * y.groups + at / kGlrGroup) * kGlrSlab + 2 * (threadIdx.x & 31);
+}
+__device__ __forceinline__ void glr_ask(GlrPiece& q, const GlrSync& y, const GlrTile& t, int warp) {
+    if (warp == kGlrGroup - 1) {
+        unsigned s0, s1;
+        asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(s0), "=r"(s1)
+                     : "l"(glr_state(y, t, t.at))
+                     : "memory");
+        q.v[0] = s0, q.v[1] = s1;
+    } else if (warp < t.at % kGlrGroup) {
+        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
+                     : "=l"(q.v[0]), "=l"(q.v[1])
+                     : "l"(glr_map(y, t, t.at / kGlrGroup * kGlrGroup + warp))
+                     : "memory");
+    } else {
+        q.v[0] = q.v[1] = 0x3f800000ull;  // no such tile: P = 1, h = 0
+    }
+}
+// The piece as (P, h) of the lane's two channels (the state as P = 0): waits
+// until both are written.  P lies in [0, 1] (or is NaN, 0x7fffffff): never the fill.
+__device__ __forceinline__ float4 glr_wait_piece(const GlrSync& y, GlrPiece q, const GlrTile& t, int warp) {
+    if ((unsigned)q.v[0] == 0xffffffffu || (unsigned)q.v[1] == 0xffffffffu) {
+        const long long t0 = clock64();
+        for (;;) {
+            glr_ask(q, y, t, warp);
+            if ((unsigned)q.v[0] != 0xffffffffu && (unsigned)q.v[1] != 0xffffffffu) break;
+            unsigned gone;
+            asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(gone) : "l"(y.ticket + 1) : "memory");
+            if (gone == 0u || clock64() - t0 > y.wait_limit) {
+                atomicExch(y.ticket + 1, 0u);
+                atomicOr(&g_glr_error, kGlrErrTimeout);
+                q.v[0] = q.v[1] = 0;
+                break;
+            }
+        }
+    }
+    if (warp == kGlrGroup - 1)
+        return make_float4(0.f, __uint_as_float((unsigned)q.v[0]), 0.f, __uint_as_float((unsigned)q.v[1]));
+    return make_float4(__uint_as_float((unsigned)q.v[0]), __uint_as_float((unsigned)(q.v[0] >> 32)),
+                       __uint_as_float((unsigned)q.v[1]), __uint_as_float((unsigned)(q.v[1] >> 32)));
+}
+// (P, h) of two channels applied to c.
+__device__ __forceinline__ float2 glr_apply(float4 q, float2 c) {
+    return glr_fma(make_float2(q.x, q.z), c, make_float2(q.y, q.w));
 }
 
-// Where a tile lies.  `at` counts tiles along the row in the order in which
-// they are walked.
-struct GlrTile {
-    unsigned rs;     // row * slabs + slab
-    int64_t at, b, len;
-    int c;           // first channel
-};
-__device__ __forceinline__ GlrTile glr_tile(const GlrParams& p, unsigned id) {
-    const unsigned slabs = (unsigned)(p.D + kGlrSlab - 1) / kGlrSlab, chains = slabs * (unsigned)p.batch;
+// The tile's first step.  BWD: tiles are walked from the row's last to its
+// first, then those past its length.
+template <bool BWD>
+__device__ __forceinline__ int64_t glr_first_step(const GlrTile& t, int tile_steps) {
+    if constexpr (!BWD) return (int64_t)t.at * tile_steps;
+    const int64_t used = ((int64_t)t.len + tile_steps - 1) / tile_steps;
+    return (t.at < used ? used - 1 - t.at : t.at) * tile_steps;
+}
+
+// The tiles of a block, in shared memory, a few ahead, each with the address
+// of its first step in every tensor.  Warp 0 looks them up (each lane one
+// tensor's address) and takes a ticket a turn before it is looked up.
+constexpr int kGlrQueue = 4;
+struct GlrEntry {
     GlrTile t;
-    t.at = id / chains;
-    t.rs = id % chains;
-    t.b = t.rs / slabs;
-    t.c = (int)(t.rs % slabs) * kGlrSlab;
-    t.len = glr_len(p, t.b);
-    return t;
+    char* at[kGlrTensors];
+};
+template <bool BWD, int ESZ>
+struct GlrQueue {
+    GlrEntry* q;
+    int tile_steps;
+    unsigned id;  // thread 0: the ticket to look up next
+    __device__ __forceinline__ unsigned ticket(const GlrSync& y) {
+        return y.ticket ? atomicAdd(y.ticket, 1u) + 1u : id + gridDim.x;
+    }
+    __device__ __forceinline__ void put(const GlrParams& p, const GlrSync& y, unsigned k) {
+        if (threadIdx.x >= 32) return;
+        GlrEntry& e = q[k % kGlrQueue];
+        const GlrTile t = glr_tile(p, y, __shfl_sync(0xffffffffu, id, 0));
+        if (threadIdx.x == 0) {
+            id = ticket(y);
+            e.t = t;
+        }
+        if (threadIdx.x < kGlrTensors && t.at >= 0) {
+            const GlrRows& r = p.rows[threadIdx.x];
+            const int64_t s = glr_first_step<BWD>(t, tile_steps);
+            // in reverse the token of step s is len - 1 - s, and ts < 0
+            const int64_t off = p.reverse ? (s - (t.len - 1)) * r.ts : s * r.ts;
+            e.at[threadIdx.x] = r.p + t.b * r.bs + off + (int64_t)glr_channel(p, t) * ESZ;
+        }
+    }
+    __device__ __forceinline__ void start(const GlrParams& p, const GlrSync& y, int n) {
+        id = blockIdx.x - gridDim.x;
+        if (threadIdx.x == 0) id = ticket(y);
+        for (int k = 0; k < n; ++k) put(p, y, k);
+        __syncthreads();
+    }
+};
+
+// The rest of a row behind its length: zeros from token t0 up to t1.
+template <typename T, bool VEC>
+__device__ __forceinline__ void glr_zero_rows(const GlrParams& p, int tensor, int64_t b, int64_t t0, int64_t t1, int c0,
+                                              int nch) {
+    const GlrRows& q = p.rows[tensor];
+    if (!q.p) return;
+    for (int64_t t = t0 + (threadIdx.x >> 5); t < t1; t += blockDim.x >> 5)
+        glr_st2<VEC>(reinterpret_cast<T*>(q.p + b * q.bs + t * (q.ts < 0 ? -(int64_t)q.ts : q.ts)) + c0,
+                     make_float2(0.f, 0.f), nch);
 }
 // Steps of a row of `len` that start at ws, at most `most`.
 __device__ __forceinline__ int glr_steps(int64_t len, int64_t ws, int most) {
@@ -359,39 +409,70 @@ __device__ __forceinline__ int glr_steps(int64_t len, int64_t ws, int most) {
 }
 
 // A warp's copy of n rows (of TOK) of one tensor into its place: row j is the
-// token t0 + step * j.  The widest copies that the launch found possible;
-// what lies past n or past the last channel becomes 0.
+// tile's step first + j, `left` channels wide.  The widest copies that the
+// launch found possible; what lies past n or past the last channel becomes 0.
 template <typename T, int TOK>
-__device__ __forceinline__ void glr_copy_rows(T* to, const GlrRows& q, const GlrTile& t, int64_t t0, int step, int n,
-                                              int D, int bytes) {
-    const int lane = threadIdx.x & 31, left = D - t.c;
-    const T* from = static_cast<const T*>(q.p) + t.b * q.bs + t0 * q.ts + t.c;
-    const int64_t ts = step * q.ts;
-    if (bytes == 16) {
+__device__ __forceinline__ void glr_copy_rows(T* to, const GlrParams& p, const GlrEntry& e, int tensor, int first, int n,
+                                              int left) {
+    const int lane = threadIdx.x & 31;
+    const char* const tile = e.at[tensor];
+    const int64_t ts = p.rows[tensor].ts;
+    if (p.copy == 16) {
         constexpr int E = 16 / sizeof(T), PER = kGlrSlab / E, ROWS = 32 / PER;  // elements a copy, copies a row
-        const int c = lane % PER * E, r = lane / PER;
-        const bool in = c < left;
+        const int col = lane % PER * E, r = lane / PER;
+        const char* from = tile + (first + r) * ts + col * sizeof(T);
+        to += r * kGlrSlab + col;
+        if (n == TOK && left >= kGlrSlab) {
 #pragma unroll
-        for (int k = 0; k < TOK / ROWS; ++k) {
-            const int j = r + k * ROWS;
-            const bool ok = in && j < n;
-            cp_async<16>(to + j * kGlrSlab + c, ok ? from + j * ts + c : static_cast<const T*>(q.p), ok);
+            for (int k = 0; k < TOK / ROWS; ++k) cp_async<16>(to + k * ROWS * kGlrSlab, from + k * ROWS * ts, true);
+        } else {
+#pragma unroll
+            for (int k = 0; k < TOK / ROWS; ++k) {
+                const bool ok = col < left && r + k * ROWS < n;
+                cp_async<16>(to + k * ROWS * kGlrSlab, ok ? from + k * ROWS * ts : tile, ok);
+            }
         }
-    } else if (bytes) {
-        const int c = 2 * lane;
+    } else if (p.copy) {
+        const int col = 2 * lane;
+        const char* from = tile + first * ts + col * sizeof(T);
 #pragma unroll 4
         for (int j = 0; j < TOK; ++j) {
-            const bool ok = c < left && j < n;
-            cp_async<2 * sizeof(T)>(to + j * kGlrSlab + c, ok ? from + j * ts + c : static_cast<const T*>(q.p), ok);
+            const bool ok = col < left && j < n;
+            cp_async<2 * sizeof(T)>(to + j * kGlrSlab + col, ok ? from + j * ts : tile, ok);
         }
     } else {
-        GlrRaw<T> v[TOK];
-        const int c = 2 * lane, nch = left - c > 1 ? 2 : (left - c > 0 ? 1 : 0);
+        T v[TOK][2];
+        const int col = 2 * lane;
+        const char* from = tile + first * ts + col * sizeof(T);
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) v[j] = glr_ld2<false>(from + j * ts + c, j < n ? nch : 0);
+        for (int j = 0; j < TOK; ++j) {
+            const T* q = reinterpret_cast<const T*>(from + j * ts);
+            v[j][0] = j < n && col < left ? q[0] : T(0.f);
+            v[j][1] = j < n && col + 1 < left ? q[1] : T(0.f);
+        }
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) *reinterpret_cast<GlrRaw<T>*>(to + j * kGlrSlab + c) = v[j];
+        for (int j = 0; j < TOK; ++j) to[j * kGlrSlab + col] = v[j][0], to[j * kGlrSlab + col + 1] = v[j][1];
     }
+}
+// Steps past a warp's last keep the state: their rows (zeros so far) get a
+// closed gate r = -inf, so that a = 1 and w = 0 without a select in the scan.
+template <typename T, int TOK>
+__device__ __forceinline__ void glr_close_rows(T* r, int n) {
+    const int lane = threadIdx.x & 31;
+    for (int j = n; j < TOK; ++j) {
+        if constexpr (sizeof(T) == 2)
+            reinterpret_cast<uint32_t*>(r + j * kGlrSlab)[lane] = 0xff80ff80u;
+        else
+            reinterpret_cast<uint2*>(r + j * kGlrSlab)[lane] = make_uint2(0xff800000u, 0xff800000u);
+    }
+}
+// -bias log2 e and A log2 e of a pair, kept finite so that a closed gate wins.
+__device__ __forceinline__ float2 glr_finite(float2 v) {
+    return make_float2(glr_max_nan(v.x, -3.4e38f), glr_max_nan(v.y, -3.4e38f));
+}
+template <bool VEC>
+__device__ __forceinline__ float2 glr_scaled(const float* v, int c, int nch, float by) {
+    return glr_finite(glr_mul(glr_vec2<VEC>(v, c, nch), glr_f2(by)));
 }
 // The lane's pair of row j.
 template <typename T>
@@ -399,165 +480,159 @@ __device__ __forceinline__ float2 glr_row(const T* rows, int j) {
     return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].get();
 }
 
-// Takes the block's first NS tiles; `slot` is shared memory.
-template <int NS>
-__device__ __forceinline__ void glr_first(const GlrSync& y, unsigned (&id)[NS], unsigned* slot) {
-    if (y.ticket) {
-        if (threadIdx.x == 0) {
-#pragma unroll
-            for (int k = 0; k < NS; ++k) slot[k] = atomicAdd(y.ticket, 1u) + 1u;
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < NS; ++k) id[k] = y.ticket ? slot[k] : blockIdx.x + k * gridDim.x;
-    __syncthreads();
-}
-
+// EPI: 0 out = h, 1 with add, 2 with z (an absent add is zero rows).
 // Stages of a block's copies: what two blocks on an SM leave room for.
-template <bool EPI>
+template <int EPI>
 constexpr int kGlrFwdStages = EPI ? 1 : 2;
-template <typename T, bool EPI>
-constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + (EPI ? 2 : 0)) * kGlrTok<T> * kGlrSlab * (int)sizeof(T);
+template <typename T, int EPI>
+constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + EPI) * kGlrTok<T> * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, bool EPI>
-__global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_fwd_kernel(const GlrParams p, const GlrSync y) {
+template <typename T, bool VEC, int EPI>
+__global__ void __launch_bounds__(kGlrWarps * 32, 2)
+    glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y) {
     constexpr int TOK = kGlrTok<T>, NS = kGlrFwdStages<EPI>, ROWS = TOK * kGlrSlab;
     extern __shared__ __align__(16) unsigned char glr_smem[];
-    __shared__ float4 aggs[2][kGlrWarps][32];
-    __shared__ float2 enter[32];
-    __shared__ unsigned slot[2];
+    __shared__ float4 aggs[2][kGlrWarps][32];      // (P, h) of each warp
+    __shared__ float4 pieces[2][kGlrGroup][32];    // what glr_ask fetched; [7] the state entering the group (or the row)
+    __shared__ GlrEntry queue[kGlrQueue];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrFwdWarpBytes<T, EPI>);
-    T* const epi = mine + 3 * NS * ROWS;
-    const int step = p.reverse ? -1 : 1;
+    T* const epi = mine + 3 * NS * ROWS;  // z, then add
     const int tile_steps = nwarp * TOK;
 
-    auto copy_inputs = [&](unsigned id, int stage) {
-        if (id < y.total) {
-            const GlrTile t = glr_tile(p, id);
-            const int64_t ws = t.at * tile_steps + warp * TOK;
-            const int n = glr_steps(t.len, ws, TOK);
-            if (n) {
-                const int64_t t0 = p.reverse ? t.len - 1 - ws : ws;
-                T* to = mine + stage * 3 * ROWS;
-                glr_copy_rows<T, TOK>(to, p.r, t, t0, step, n, p.D, p.copy);
-                glr_copy_rows<T, TOK>(to + ROWS, p.i, t, t0, step, n, p.D, p.copy);
-                glr_copy_rows<T, TOK>(to + 2 * ROWS, p.x, t, t0, step, n, p.D, p.copy);
-            }
+    auto copy_inputs = [&](const GlrEntry& e, int stage) {
+        const GlrTile t = e.t;
+        const int n = t.at < 0 ? 0 : glr_steps(t.len, (int64_t)t.at * tile_steps + warp * TOK, TOK);
+        if (n) {
+            const int left = p.D - glr_channel(p, t);
+            T* to = mine + stage * 3 * ROWS;
+            glr_copy_rows<T, TOK>(to, p, e, kGlrR, warp * TOK, n, left);
+            glr_copy_rows<T, TOK>(to + ROWS, p, e, kGlrI, warp * TOK, n, left);
+            glr_copy_rows<T, TOK>(to + 2 * ROWS, p, e, kGlrX, warp * TOK, n, left);
         }
         cp_async_commit();
     };
 
-    unsigned ids[NS];
-    glr_first<NS>(y, ids, slot);
+    GlrQueue<false, sizeof(T)> tiles{queue, tile_steps};
+    tiles.start(p, y, NS);
+    if (EPI == 2 && !p.rows[kGlrAdd].p) {
+        for (int j = lane; j < ROWS; j += 32) epi[ROWS + j] = T(0.f);
+    }
 #pragma unroll
-    for (int k = 0; k < NS; ++k) copy_inputs(ids[k], k);
-    int stage = 0, par = 0;
-    while (ids[0] < y.total) {
-        const GlrTile t = glr_tile(p, ids[0]);
-        unsigned ahead = ids[NS - 1] + gridDim.x;
-        if (y.ticket && threadIdx.x == 0) ahead = atomicAdd(y.ticket, 1u) + 1u;
-        const int c0 = t.c + 2 * lane;
+    for (int k = 0; k < NS; ++k) copy_inputs(queue[k], k);
+    for (unsigned k = 0;; ++k) {
+        const GlrEntry& e = queue[k % kGlrQueue];
+        GlrTile t = e.t;
+        if (t.at < 0) break;
+        tiles.put(p, y, k + NS);  // over entry k + NS - 4, which every warp has left behind
+        const int stage = NS == 2 ? k & 1 : 0;
+        const int c0 = glr_channel(p, t) + 2 * lane;
         const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
-        const int64_t b = t.b, len = t.len, s0 = t.at * tile_steps, s1 = s0 + tile_steps;  // the tile's steps [s0, s1)
-        const int64_t ws = s0 + warp * TOK;
-        const int n = glr_steps(len, ws, TOK);
-        const int64_t t0 = p.reverse ? len - 1 - ws : ws;  // the token of the warp's first step
-        if (len < s1) glr_zero_rows<T, VEC>(p.out, b, len > s0 ? len : s0, s1 < p.L ? s1 : p.L, c0, nch, warp, nwarp);
-        if (len == 0 && s0 == 0 && warp == 0 && p.h_out)
-            glr_put2(p.h_out + b * p.D + c0, glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch), nch);
-        float4(*agg)[32] = aggs[par];
+        const int64_t s0 = (int64_t)t.at * tile_steps, s1 = s0 + tile_steps;  // the tile's steps [s0, s1)
+        const int64_t ws = s0 + warp * TOK, row = (int64_t)t.b * p.D + c0;
+        const int n = glr_steps(t.len, ws, TOK);
+        const bool active = t.len > s0;
+        if (t.len < s1)
+            glr_zero_rows<T, VEC>(p, kGlrOut, t.b, t.len > s0 ? t.len : s0, s1 < p.L ? s1 : p.L, c0, nch);
+        if (t.len == 0 && t.at == 0 && warp == 0 && p.h_out)
+            glr_st2<VEC>(p.h_out + row, glr_vec2<VEC>(p.h_in, row, nch), nch);
+        GlrPiece piece;
+        if (active && t.at) glr_ask(piece, y, t, warp);
+        float4(*agg)[32] = aggs[k & 1];
+        float4(*got)[32] = pieces[k & 1];
         float2 Ps[TOK], hs[TOK];
         cp_async_wait_pending<NS - 1>();
         __syncwarp();
-        if constexpr (EPI) {
-            // every lane is past its last tile's phase 2
-            if (n && p.add.p) glr_copy_rows<T, TOK>(epi, p.add, t, t0, step, n, p.D, p.copy);
-            if (n && p.z.p) glr_copy_rows<T, TOK>(epi + ROWS, p.z, t, t0, step, n, p.D, p.copy);
+        if constexpr (EPI > 0) {
+            // every lane is past its last tile's outputs
+            const int left = p.D - (c0 - 2 * lane);
+            if (EPI == 2 && n) glr_copy_rows<T, TOK>(epi, p, e, kGlrZ, warp * TOK, n, left);
+            if (n && p.rows[kGlrAdd].p)
+                glr_copy_rows<T, TOK>(epi + (EPI - 1) * ROWS, p, e, kGlrAdd, warp * TOK, n, left);
             cp_async_commit();
         }
-        {
-            const T* in = mine + stage * 3 * ROWS;
-            const float2 A2 = glr_mul(glr_vec2(p.A + c0, nch), glr_f2(kGlrLog2e));
-            const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-            const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
+        if (n) {
+            T* in = mine + stage * 3 * ROWS;
+            if (n < TOK) glr_close_rows<T, TOK>(in, n);
+            const float2 A2 = glr_scaled<VEC>(p.A, c0, nch, kGlrLog2e);
+            const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
+            const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
             float2 P = glr_f2(1.f), h = glr_f2(0.f);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
-                float2 a = g.a, w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in + 2 * ROWS, j));
-                if (j >= n) a = glr_f2(1.f), w = glr_f2(0.f);  // past the end: the state stays
-                P = glr_mul(P, a);
-                h = glr_fma(a, h, w);
+                const float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in + 2 * ROWS, j));
+                P = glr_mul(P, g.a);
+                h = glr_fma(g.a, h, w);
                 Ps[j] = P;
                 hs[j] = h;
             }
             agg[warp][lane] = make_float4(P.x, h.x, P.y, h.y);
+        } else {
+            agg[warp][lane] = make_float4(1.f, 0.f, 1.f, 0.f);
         }
-        if (threadIdx.x == 0) slot[par] = ahead;
+        if (t.at == 0 && warp == nwarp - 1) {
+            const float2 c = glr_vec2<VEC>(p.h_in, row, nch);
+            got[kGlrGroup - 1][lane] = make_float4(0.f, c.x, 0.f, c.y);
+        }
         __syncthreads();
-        ahead = slot[par];
-        if (len > s0 && warp == 0) {
-            float2 P = glr_f2(1.f), h = glr_f2(0.f);
+        t = e.t;  // (read again rather than kept)
+        if (!active) {
+            copy_inputs(queue[(k + NS) % kGlrQueue], stage);
+            continue;
+        }
+        const bool last = s1 >= t.len, publish = y.ticket && !last && !y.starve;
+        float2 P = glr_f2(1.f), h = glr_f2(0.f);
+        if (warp == 0) {
             for (int w = 0; w < nwarp; ++w) {
                 const float4 q = agg[w][lane];
-                const float2 Pw = make_float2(q.x, q.z);
-                P = glr_mul(P, Pw);
-                h = glr_fma(Pw, h, make_float2(q.y, q.w));
+                P = glr_mul(P, make_float2(q.x, q.z));
+                h = glr_apply(q, h);
             }
-            const bool last = s1 >= len, publish = y.ticket && !last && !y.starve;
-            unsigned long long* map = y.map + (int64_t)t.rs * y.tiles * kGlrSlab + 2 * lane;
-            float* state = y.state + (int64_t)t.rs * y.groups * kGlrSlab + 2 * lane;
-            if (publish) glr_publish_map(map + t.at * kGlrSlab, P, h);
-            float2 c;
-            if (t.at == 0) {
-                // the other tiles take it from here, not from h_in, which may be h_out
-                c = glr_vec2(p.h_in ? p.h_in + b * p.D + c0 : nullptr, nch);
-                if (publish) glr_publish_state(state, c);
-            } else {
-                c = glr_lookback(y, map, state, t.at);
-            }
-            enter[lane] = c;
-            const float2 end = glr_fma(P, c, h);
-            if (publish && (t.at + 1) % kGlrGroup == 0) glr_publish_state(state + (t.at + 1) / kGlrGroup * kGlrSlab, end);
-            if (last && p.h_out) glr_put2(p.h_out + b * p.D + c0, end, nch);
+            if (publish) glr_publish_map(glr_map(y, t, t.at), P, h);
         }
-        copy_inputs(ahead, stage);
-        if (len > s0) {
+        if (t.at) {
+            got[warp][lane] = glr_wait_piece(y, piece, t, warp);
             __syncthreads();
-            float2 c = enter[lane];
-            for (int w = 0; w < warp; ++w) {
-                const float4 q = agg[w][lane];
-                c = glr_fma(make_float2(q.x, q.z), c, make_float2(q.y, q.w));
-            }
-            if (p.chunk && n > 0 && ws % kGlrChunk == 0)
-                glr_put2(p.chunk + (b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
-            if constexpr (EPI) {
-                cp_async_wait_pending<1>();  // all but the next tile's inputs
-                __syncwarp();
-            }
-            T* po = static_cast<T*>(p.out.p) + b * p.out.bs + t0 * p.out.ts + c0;
-            const int64_t ao = step * p.out.ts;
+        }
+        const float4 from = got[kGlrGroup - 1][lane];
+        float2 c = make_float2(from.y, from.w);
+        for (int w = 0; w < t.at % kGlrGroup; ++w) c = glr_apply(got[w][lane], c);
+        if (warp == 0) {
+            const float2 end = glr_fma(P, c, h);
+            // the other tiles take a row's first state from here, not from h_in, which may be h_out
+            if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
+            if (publish && (t.at + 1) % kGlrGroup == 0)
+                glr_publish_state(glr_state(y, t, t.at + 1), end);
+            if (last && p.h_out) glr_st2<VEC>(p.h_out + row, end, nch);
+        }
+        for (int w = 0; w < warp; ++w) c = glr_apply(agg[w][lane], c);
+        copy_inputs(queue[(k + NS) % kGlrQueue], stage);
+        if (p.chunk && n > 0 && ws % kGlrChunk == 0)
+            glr_st2<VEC>(p.chunk + ((int64_t)t.b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
+        if constexpr (EPI > 0) {
+            cp_async_wait_pending<1>();  // all but the next tile's inputs
+            __syncwarp();
+        }
+        const int64_t ts = p.rows[kGlrOut].ts;
+        char* po = e.at[kGlrOut] + warp * TOK * ts + 2 * lane * (int)sizeof(T);
+        auto outputs = [&](auto full) {
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 float2 h = glr_fma(Ps[j], c, hs[j]);
-                if constexpr (EPI) {
-                    if (p.add.p) h = glr_add(h, glr_row(epi, j));
-                    if (p.z.p) {
-                        const float2 z = glr_row(epi + ROWS, j);
-                        h = glr_mul(h, glr_mul(z, glr_sigmoid2(z)));
-                    }
+                if constexpr (EPI > 0) h = glr_add(h, glr_row(epi + (EPI - 1) * ROWS, j));
+                if constexpr (EPI == 2) {
+                    const float2 z = glr_row(epi, j);
+                    h = glr_mul(h, glr_mul(z, glr_sigmoid2(z)));
                 }
-                glr_st2<VEC>(po + j * ao, h, j < n ? nch : 0);
+                if (decltype(full)::value || j < n) glr_st2<VEC>(reinterpret_cast<T*>(po), h, nch);
+                po += ts;
             }
-        }
-        par ^= 1;
-        if constexpr (NS == 2) {
-            ids[0] = ids[1];
-            stage ^= 1;
-        }
-        ids[NS - 1] = ahead;
+        };
+        if (n == TOK)
+            outputs(std::true_type{});
+        else
+            outputs(std::false_type{});
     }
     cp_async_wait_all();
 }
@@ -572,217 +647,221 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_fwd_kernel(const G
 constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
 template <typename T>
 constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
-template <typename T, bool EPI>
-constexpr int kGlrBwdWarpBytes = (EPI ? 6 : 4) * kGlrBwdStages<T> * kGlrBwdTok * kGlrSlab * (int)sizeof(T);
+template <typename T, int EPI>
+constexpr int kGlrBwdWarpBytes = (EPI == 2 ? 6 : 4) * kGlrBwdStages<T> * kGlrBwdTok * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, bool EPI>
-__global__ void __launch_bounds__(kGlrWarps * 32, 2) glr_tile_bwd_kernel(const GlrParams p, const GlrSync y) {
-    constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI ? 6 : 4;
+template <typename T, bool VEC, int EPI>
+__global__ void __launch_bounds__(kGlrWarps * 32, 2)
+    glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y) {
+    constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI == 2 ? 6 : 4;
     extern __shared__ __align__(16) unsigned char glr_smem[];
-    __shared__ float2 aggP[kGlrWarps][32], aggh[kGlrWarps][32], aggq[kGlrWarps][32];
+    __shared__ float4 agg[kGlrWarps][32];   // (P, q) of each warp
+    __shared__ float2 aggh[kGlrWarps][32];  // its h
+    __shared__ float4 pieces[kGlrGroup][32];
     __shared__ float2 sums[3][kGlrWarps][32];
-    __shared__ float2 enter[32];
-    __shared__ unsigned slot[2];
+    __shared__ GlrEntry queue[kGlrQueue];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrBwdWarpBytes<T, EPI>);
-    const int step = p.reverse ? -1 : 1;
-    const float2 one = glr_f2(1.f), minus = glr_f2(-1.f);
 
-    // the tile's place along the row, in steps' order
-    auto index_of = [](const GlrTile& t) {
-        const int64_t used = (t.len + kGlrChunk - 1) / kGlrChunk;  // the row's own tiles
-        return t.at < used ? used - 1 - t.at : t.at;
-    };
-    auto copy_inputs = [&](unsigned id, int stage) {
-        if (id < y.total) {
-            const GlrTile t = glr_tile(p, id);
-            const int64_t ws = index_of(t) * kGlrChunk + warp * TOK;
-            const int n = glr_steps(t.len, ws, TOK);
-            if (n) {
-                const int64_t t0 = p.reverse ? t.len - 1 - ws : ws;
-                T* to = mine + stage * NT * ROWS;
-                glr_copy_rows<T, TOK>(to, p.r, t, t0, step, n, p.D, p.copy);
-                glr_copy_rows<T, TOK>(to + ROWS, p.i, t, t0, step, n, p.D, p.copy);
-                glr_copy_rows<T, TOK>(to + 2 * ROWS, p.x, t, t0, step, n, p.D, p.copy);
-                glr_copy_rows<T, TOK>(to + 3 * ROWS, p.dout, t, t0, step, n, p.D, p.copy);
-                if (EPI && p.add.p) glr_copy_rows<T, TOK>(to + 4 * ROWS, p.add, t, t0, step, n, p.D, p.copy);
-                if (EPI && p.z.p) glr_copy_rows<T, TOK>(to + 5 * ROWS, p.z, t, t0, step, n, p.D, p.copy);
+    auto copy_inputs = [&](const GlrEntry& e, int stage) {
+        const GlrTile t = e.t;
+        const int n = t.at < 0 ? 0 : glr_steps(t.len, glr_first_step<true>(t, kGlrChunk) + warp * TOK, TOK);
+        if (n) {
+            const int left = p.D - glr_channel(p, t);
+            T* to = mine + stage * NT * ROWS;
+            glr_copy_rows<T, TOK>(to, p, e, kGlrR, warp * TOK, n, left);
+            glr_copy_rows<T, TOK>(to + ROWS, p, e, kGlrI, warp * TOK, n, left);
+            glr_copy_rows<T, TOK>(to + 2 * ROWS, p, e, kGlrX, warp * TOK, n, left);
+            glr_copy_rows<T, TOK>(to + 3 * ROWS, p, e, kGlrDout, warp * TOK, n, left);
+            if constexpr (EPI == 2) {
+                glr_copy_rows<T, TOK>(to + 4 * ROWS, p, e, kGlrZ, warp * TOK, n, left);
+                if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK>(to + 5 * ROWS, p, e, kGlrAdd, warp * TOK, n, left);
             }
         }
         cp_async_commit();
     };
-
-    unsigned ids[NS];
-    glr_first<NS>(y, ids, slot);
+    // the parameters' sums of the tile before, once a barrier has passed
+    float* part = nullptr;
+    int part_n = 0;
+    auto put_sums = [&]() {
+        if (part_n && warp < 3) {
+            float2 v = glr_f2(0.f);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) copy_inputs(ids[k], k);
-    int stage = 0, par = 0;
-    while (ids[0] < y.total) {
-        const GlrTile t = glr_tile(p, ids[0]);
-        unsigned ahead = ids[NS - 1] + gridDim.x;
-        if (y.ticket && threadIdx.x == 0) ahead = atomicAdd(y.ticket, 1u) + 1u;
-        const int c0 = t.c + 2 * lane;
+            for (int w = 0; w < kGlrWarps; ++w) v = glr_add(v, sums[warp][w][lane]);
+            glr_st2<VEC>(part + (int64_t)warp * p.D, v, part_n);
+        }
+    };
+
+    GlrQueue<true, sizeof(T)> tiles{queue, kGlrChunk};
+    tiles.start(p, y, NS);
+    if (EPI == 2 && !p.rows[kGlrAdd].p) {
+        for (int k = 0; k < NS; ++k)
+            for (int j = lane; j < ROWS; j += 32) mine[(k * NT + 5) * ROWS + j] = T(0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < NS; ++k) copy_inputs(queue[k], k);
+    for (unsigned k = 0;; ++k) {
+        const GlrEntry& e = queue[k % kGlrQueue];
+        GlrTile t = e.t;
+        if (t.at < 0) break;
+        tiles.put(p, y, k + NS);  // over entry k + NS - 4, which every warp has left behind
+        const int stage = NS == 2 ? k & 1 : 0;
+        const int c0 = glr_channel(p, t) + 2 * lane;
         const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
-        const int64_t b = t.b, len = t.len, ti = index_of(t), s0 = ti * kGlrChunk, s1 = s0 + kGlrChunk;
-        const int64_t ws = s0 + warp * TOK;
-        const int n = glr_steps(len, ws, TOK);
-        const int64_t t0 = p.reverse ? len - 1 - ws : ws;
-        float* part = p.part + (b * p.nchunk + ti) * 3 * p.D + c0;
-        if (len < s1) {
-            const int64_t z0 = len > s0 ? len : s0, z1 = s1 < p.L ? s1 : p.L;
-            glr_zero_rows<T, VEC>(p.dx, b, z0, z1, c0, nch, warp, kGlrWarps);
-            glr_zero_rows<T, VEC>(p.dr, b, z0, z1, c0, nch, warp, kGlrWarps);
-            glr_zero_rows<T, VEC>(p.di, b, z0, z1, c0, nch, warp, kGlrWarps);
-            if (EPI && p.add.p) glr_zero_rows<T, VEC>(p.dadd, b, z0, z1, c0, nch, warp, kGlrWarps);
-            if (EPI && p.z.p) glr_zero_rows<T, VEC>(p.dz, b, z0, z1, c0, nch, warp, kGlrWarps);
+        const int64_t s0 = glr_first_step<true>(t, kGlrChunk), s1 = s0 + kGlrChunk, row = (int64_t)t.b * p.D + c0;
+        const int64_t chunk = ((int64_t)t.b * p.nchunk + s0 / kGlrChunk) * p.D;
+        const int n = glr_steps(t.len, s0 + warp * TOK, TOK);
+        const bool active = t.len > s0;
+        if (t.len < s1) {
+            const int64_t z0 = t.len > s0 ? t.len : s0, z1 = s1 < p.L ? s1 : p.L;
+            for (int q = kGlrDx; q <= kGlrDz; ++q) glr_zero_rows<T, VEC>(p, q, t.b, z0, z1, c0, nch);
         }
-        const bool active = len > s0;
-        if (!active) {
-            if (warp < 3) glr_put2(part + (int64_t)warp * p.D, glr_f2(0.f), nch);
-            if (t.at == 0 && warp == 0 && p.dh_in)
-                glr_put2(p.dh_in + b * p.D + c0, glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch), nch);
-        }
-        const T* in = mine + stage * NT * ROWS;
-        const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_add = in + 4 * ROWS, *in_z = in + 5 * ROWS;
+        if (!active && t.at == 0 && warp == 0 && p.dh_in)
+            glr_st2<VEC>(p.dh_in + row, glr_vec2<VEC>(p.dh_out, row, nch), nch);
+        GlrPiece piece;
+        if (active && t.at) glr_ask(piece, y, t, warp);
+        T* in = mine + stage * NT * ROWS;
+        const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_z = in + 4 * ROWS, *in_add = in + 5 * ROWS;
         float2 rg[TOK], ig[TOK], u[TOK], hp[TOK];
-        const float2 A = glr_vec2(p.A + c0, nch);
         float2 entering = glr_f2(0.f);
-        if (active) entering = glr_vec2(p.chunk + (b * p.nchunk + ti) * p.D + c0, nch);
+        if (active) entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
         cp_async_wait_pending<NS - 1>();
         __syncwarp();
-        {
-            const float2 nr = glr_mul(glr_vec2(p.r_bias ? p.r_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-            const float2 ni = glr_mul(glr_vec2(p.i_bias ? p.i_bias + c0 : nullptr, nch), glr_f2(-kGlrLog2e));
-            const float2 A2 = glr_mul(A, glr_f2(kGlrLog2e));
-            float2 P = one, h = glr_f2(0.f);
+        float2 P = glr_f2(1.f), q = glr_f2(0.f), h = glr_f2(0.f);
+        if (n) {
+            if (n < TOK) glr_close_rows<T, TOK>(in, n);
+            const float2 A2 = glr_scaled<VEC>(p.A, c0, nch, kGlrLog2e);
+            const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
+            const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
-                float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in_x, j)), a = g.a;
+                const float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in_x, j));
                 rg[j] = g.rg;
                 ig[j] = make_float2(glr_rcp(g.di.x), glr_rcp(g.di.y));
                 u[j] = g.u;
-                if (j >= n) a = one, u[j] = w = glr_f2(0.f);
                 hp[j] = h;  // the state before step j, from a zero state at the warp's first
-                P = glr_mul(P, a);
-                h = glr_fma(a, h, w);
+                P = glr_mul(P, g.a);
+                h = glr_fma(g.a, h, w);
             }
-            float2 q = glr_f2(0.f);
 #pragma unroll
             for (int j = TOK - 1; j >= 0; --j) {
                 float2 dh = glr_row(in_d, j);
-                if constexpr (EPI) {
-                    if (p.z.p) {
-                        const float2 z = glr_row(in_z, j);
-                        dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
-                    }
+                if constexpr (EPI == 2) {
+                    const float2 z = glr_row(in_z, j);
+                    dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
                 }
-                if (j >= n) dh = glr_f2(0.f);
                 const float2 G = glr_add(q, dh);
-                q = glr_fma(u[j], glr_mul(G, minus), G);  // a G; past the end u is 0
+                q = glr_sub(G, glr_mul(u[j], G));  // a G
             }
-            aggP[warp][lane] = P;
-            aggh[warp][lane] = h;
-            aggq[warp][lane] = q;
         }
-        if (threadIdx.x == 0) slot[par] = ahead;
+        aggh[warp][lane] = h;
+        agg[warp][lane] = make_float4(P.x, q.x, P.y, q.y);
         __syncthreads();
-        ahead = slot[par];
+        t = e.t;  // (read again rather than kept)
+        put_sums();
+        part = p.part + chunk * 3 + c0;
+        part_n = nch;
+        float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
         if (active) {
-            if (warp == 0) {
-                float2 P = one, q = glr_f2(0.f);
-                for (int w = kGlrWarps - 1; w >= 0; --w) {
-                    P = glr_mul(P, aggP[w][lane]);
-                    q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
-                }
-                const bool last = ti == 0, publish = y.ticket && !last && !y.starve;
-                unsigned long long* map = y.map + (int64_t)t.rs * y.tiles * kGlrSlab + 2 * lane;
-                float* state = y.state + (int64_t)t.rs * y.groups * kGlrSlab + 2 * lane;
-                if (publish) glr_publish_map(map + t.at * kGlrSlab, P, q);
-                float2 c;
-                if (t.at == 0) {
-                    c = glr_vec2(p.dh_out ? p.dh_out + b * p.D + c0 : nullptr, nch);
-                    if (publish) glr_publish_state(state, c);
-                } else {
-                    c = glr_lookback(y, map, state, t.at);
-                }
-                enter[lane] = c;
-                const float2 end = glr_fma(P, c, q);
-                if (publish && (t.at + 1) % kGlrGroup == 0)
-                    glr_publish_state(state + (t.at + 1) / kGlrGroup * kGlrSlab, end);
-                if (last && p.dh_in) glr_put2(p.dh_in + b * p.D + c0, end, nch);
+            const bool last = s0 == 0, publish = y.ticket && !last && !y.starve;
+            // the map from the tile's end to the warp's, and for warp 0 to the tile's start
+            float2 Pw = glr_f2(1.f), qw = glr_f2(0.f);
+            for (int w = kGlrWarps - 1; w > warp; --w) {
+                const float4 a = agg[w][lane];
+                Pw = glr_mul(Pw, make_float2(a.x, a.z));
+                qw = glr_apply(a, qw);
             }
-            {
-                // the states before the warp's steps, from the one that enters the tile
+            q = glr_fma(P, qw, q);
+            P = glr_mul(P, Pw);
+            if (publish && warp == 0) glr_publish_map(glr_map(y, t, t.at), P, q);
+            float4 mypiece = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t.at) {
+                mypiece = glr_wait_piece(y, piece, t, warp);
+            } else if (warp == kGlrGroup - 1) {
+                const float2 c = glr_vec2<VEC>(p.dh_out, row, nch);
+                mypiece = make_float4(0.f, c.x, 0.f, c.y);
+            }
+            pieces[warp][lane] = mypiece;
+            // the states before the warp's steps, from the one that enters the tile
+            if (n) {
                 float2 c = entering;
-                for (int w = 0; w < warp; ++w) c = glr_fma(aggP[w][lane], c, aggh[w][lane]);
+                for (int w = 0; w < warp; ++w) {
+                    const float4 a = agg[w][lane];
+                    c = glr_fma(make_float2(a.x, a.z), c, aggh[w][lane]);
+                }
 #pragma unroll
                 for (int j = 0; j < TOK; ++j) {
                     hp[j] = glr_add(c, hp[j]);
-                    c = glr_fma(u[j], glr_mul(c, minus), c);
+                    c = glr_sub(c, glr_mul(u[j], c));
                 }
             }
             __syncthreads();
-            float2 q = enter[lane];
-            for (int w = kGlrWarps - 1; w > warp; --w) q = glr_fma(aggP[w][lane], q, aggq[w][lane]);
-            float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
+            const float4 from = pieces[kGlrGroup - 1][lane];
+            float2 c = make_float2(from.y, from.w);
+            for (int w = 0; w < t.at % kGlrGroup; ++w) c = glr_apply(pieces[w][lane], c);
+            if (warp == 0) {
+                const float2 end = glr_fma(P, c, q);
+                // the other tiles take the last state's gradient from here, not from dh_out, which may be dh_in
+                if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
+                if (publish && (t.at + 1) % kGlrGroup == 0)
+                    glr_publish_state(glr_state(y, t, t.at + 1), end);
+                if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
+            }
+            q = glr_fma(Pw, c, qw);
+            const float2 A = glr_vec2<VEC>(p.A, c0, nch);
+            const int col = 2 * lane * (int)sizeof(T);
+            auto to = [&](int tensor, int j) {
+                const int64_t ts = p.rows[tensor].ts;
+                return reinterpret_cast<T*>(e.at[tensor] + (warp * TOK + j) * ts + col);
+            };
+            auto outputs = [&](auto full) {
 #pragma unroll
-            for (int j = TOK - 1; j >= 0; --j) {
-                const int m = j < n ? nch : 0;
-                const int64_t tk = t0 + step * j;
-                const float2 a = glr_fma(u[j], minus, one), b2 = glr_mul(u[j], glr_add(a, one));
-                const float2 b2t = glr_add(b2, glr_f2(kGlrTiny));
-                const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
-                const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
-                float2 dh = glr_row(in_d, j);
-                if constexpr (EPI) {
-                    if (p.z.p) {
+                for (int j = TOK - 1; j >= 0; --j) {
+                    if (!decltype(full)::value && j >= n) continue;
+                    const float2 a = glr_one_minus(u[j]), b2 = glr_mul(u[j], glr_add(a, 1.f));
+                    const float2 b2t = glr_add(b2, kGlrTiny);
+                    const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
+                    const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
+                    float2 dh = glr_row(in_d, j);
+                    if constexpr (EPI == 2) {
                         const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
-                        float2 h = glr_fma(a, hp[j], w);
-                        if (p.add.p) h = glr_add(h, glr_row(in_add, j));
+                        const float2 h = glr_add(glr_fma(a, hp[j], w), glr_row(in_add, j));
                         // silu'(z) = s (1 + z (1 - s))
-                        const float2 ds = glr_mul(sz, glr_fma(z, glr_fma(sz, minus, one), one));
-                        glr_st2<VEC>(static_cast<T*>(p.dz.p) + b * p.dz.bs + tk * p.dz.ts + c0,
-                                     glr_mul(glr_mul(dh, h), ds), m);
+                        const float2 ds = glr_mul(sz, glr_fma(z, glr_one_minus(sz), 1.f));
+                        glr_st2<VEC>(to(kGlrDz, j), glr_mul(glr_mul(dh, h), ds), nch);
                         dh = glr_mul(dh, glr_mul(z, sz));
                     }
-                    if (p.add.p) glr_st2<VEC>(static_cast<T*>(p.dadd.p) + b * p.dadd.bs + tk * p.dadd.ts + c0, dh, m);
+                    if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) glr_st2<VEC>(to(kGlrDadd, j), dh, nch);
+                    const float2 G = glr_add(dh, q);
+                    q = glr_mul(a, G);
+                    const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
+                    const float2 dla = glr_mul(G, glr_sub(glr_mul(a, hp[j]), glr_mul(glr_mul(ab, ab), w)));
+                    const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_one_minus(rg[j])));
+                    const float2 di = glr_mul(glr_mul(G, w), glr_one_minus(ig[j]));
+                    glr_st2<VEC>(to(kGlrDx, j), glr_mul(G, bi), nch);
+                    glr_st2<VEC>(to(kGlrDr, j), dr, nch);
+                    glr_st2<VEC>(to(kGlrDi, j), di, nch);
+                    sA = glr_fma(rg[j], dla, sA);
+                    sr = glr_add(sr, dr);
+                    si = glr_add(si, di);
                 }
-                if (j >= n) continue;
-                const float2 G = glr_add(dh, q);
-                q = glr_mul(a, G);
-                const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
-                const float2 dla = glr_mul(G, glr_fma(a, hp[j], glr_mul(glr_mul(ab, ab), glr_mul(w, minus))));
-                const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_fma(rg[j], minus, one)));
-                const float2 di = glr_mul(glr_mul(G, w), glr_fma(ig[j], minus, one));
-                glr_st2<VEC>(static_cast<T*>(p.dx.p) + b * p.dx.bs + tk * p.dx.ts + c0, glr_mul(G, bi), m);
-                glr_st2<VEC>(static_cast<T*>(p.dr.p) + b * p.dr.bs + tk * p.dr.ts + c0, dr, m);
-                glr_st2<VEC>(static_cast<T*>(p.di.p) + b * p.di.bs + tk * p.di.ts + c0, di, m);
-                sA = glr_fma(rg[j], dla, sA);
-                sr = glr_add(sr, dr);
-                si = glr_add(si, di);
-            }
-            sums[0][warp][lane] = sA;
-            sums[1][warp][lane] = sr;
-            sums[2][warp][lane] = si;
+            };
+            if (n == TOK)
+                outputs(std::true_type{});
+            else
+                outputs(std::false_type{});
+        } else {
+            __syncthreads();  // the sums of the tile before are read
         }
+        sums[0][warp][lane] = sA;
+        sums[1][warp][lane] = sr;
+        sums[2][warp][lane] = si;
         __syncwarp();  // every lane has read its rows
-        copy_inputs(ahead, stage);
-        if (active) {
-            __syncthreads();
-            if (warp < 3) {
-                float2 v = glr_f2(0.f);
-                for (int w = 0; w < kGlrWarps; ++w) v = glr_add(v, sums[warp][w][lane]);
-                glr_put2(part + (int64_t)warp * p.D, v, nch);
-            }
-        }
-        par ^= 1;
-        if constexpr (NS == 2) {
-            ids[0] = ids[1];
-            stage ^= 1;
-        }
-        ids[NS - 1] = ahead;
+        copy_inputs(queue[(k + NS) % kGlrQueue], stage);
     }
+    __syncthreads();
+    put_sums();
     cp_async_wait_all();
 }
 

@@ -20,17 +20,18 @@ bool sizes_ok(int batch, int64_t L, int D) {
     return batch > 0 && batch <= kMaxBatch && L > 0 && L <= 0x7fffffffLL && D > 0;
 }
 
-// Rows that are read: any strides from 0.
-int check_in(const bimamba_rows_t& q, size_t esz, bool optional) {
+// Rows that are read: any strides from 0; the kernels step through a row in 32 bits.
+int check_in(const bimamba_rows_t& q, size_t esz, int64_t L, bool optional) {
     if (!q.ptr) return optional ? BIMAMBA_OK : BIMAMBA_ERR_INVALID_ARG;
     if (q.batch_stride < 0 || q.token_stride < 0) return BIMAMBA_ERR_INVALID_ARG;
+    if (L > 1 && q.token_stride > BIMAMBA_GLR_MAX_TOKEN_STRIDE) return BIMAMBA_ERR_UNSUPPORTED;
     return aligned(q.ptr, esz) ? BIMAMBA_OK : BIMAMBA_ERR_MISALIGNED;
 }
 
 // Rows that are written: no two of them may overlap, so the strides have to
 // nest one way or the other ([batch][L] or [L][batch] order).
 int check_out(const bimamba_rows_t& q, size_t esz, int batch, int64_t L, int D) {
-    int rc = check_in(q, esz, false);
+    int rc = check_in(q, esz, L, false);
     if (rc) return rc;
     const bool tok = L == 1 || q.token_stride >= D, bat = batch == 1 || q.batch_stride >= D;
     if (!tok || !bat) return BIMAMBA_ERR_INVALID_ARG;
@@ -42,19 +43,17 @@ int check_out(const bimamba_rows_t& q, size_t esz, int batch, int64_t L, int D) 
     return BIMAMBA_OK;
 }
 
-GlrRows rows(const bimamba_rows_t& q) { return {q.ptr, q.batch_stride, q.token_stride}; }
-
 int check_common(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, int batch, int64_t L, int D,
                  unsigned flags) {
     if (!in || !p || !sizes_ok(batch, L, D)) return BIMAMBA_ERR_INVALID_ARG;
     if (flags & ~(BIMAMBA_GLR_REVERSE | BIMAMBA_TEST_STARVE)) return BIMAMBA_ERR_UNSUPPORTED;
     if (!dtype_ok(in->dtype)) return BIMAMBA_ERR_UNSUPPORTED;
     const size_t e = elem_size(in->dtype);
-    int rc = check_in(in->x, e, false);
-    if (!rc) rc = check_in(in->r, e, false);
-    if (!rc) rc = check_in(in->i, e, false);
-    if (!rc) rc = check_in(in->add, e, true);
-    if (!rc) rc = check_in(in->z, e, true);
+    int rc = check_in(in->x, e, L, false);
+    if (!rc) rc = check_in(in->r, e, L, false);
+    if (!rc) rc = check_in(in->i, e, L, false);
+    if (!rc) rc = check_in(in->add, e, L, true);
+    if (!rc) rc = check_in(in->z, e, L, true);
     if (rc) return rc;
     if (!p->A) return BIMAMBA_ERR_INVALID_ARG;
     if (!aligned(p->A, 4) || !aligned(p->r_bias, 4) || !aligned(p->i_bias, 4) || !aligned(in->lengths, 4))
@@ -62,13 +61,14 @@ int check_common(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, 
     return BIMAMBA_OK;
 }
 
+// Strides in bytes, the token's with the sign of the walk (0 where there is one token).
+void set_rows(GlrParams& k, int tensor, const bimamba_rows_t& q, size_t esz) {
+    const int ts = k.L > 1 ? (int)(q.token_stride * (int64_t)esz) : 0;
+    k.rows[tensor] = {static_cast<char*>(q.ptr), q.batch_stride * (int64_t)esz, k.reverse ? -ts : ts};
+}
+
 void fill_common(GlrParams& k, const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, int batch, int64_t L,
                  int D, unsigned flags) {
-    k.x = rows(in->x);
-    k.r = rows(in->r);
-    k.i = rows(in->i);
-    k.add = rows(in->add);
-    k.z = rows(in->z);
     k.lengths = in->lengths;
     k.A = p->A;
     k.r_bias = p->r_bias;
@@ -78,6 +78,12 @@ void fill_common(GlrParams& k, const bimamba_glr_inputs_t* in, const bimamba_glr
     k.batch = batch;
     k.reverse = (flags & BIMAMBA_GLR_REVERSE) ? 1 : 0;
     k.nchunk = (L + bimamba::kGlrChunk - 1) / bimamba::kGlrChunk;
+    const size_t e = elem_size(in->dtype);
+    set_rows(k, bimamba::kGlrX, in->x, e);
+    set_rows(k, bimamba::kGlrR, in->r, e);
+    set_rows(k, bimamba::kGlrI, in->i, e);
+    if (in->add.ptr) set_rows(k, bimamba::kGlrAdd, in->add, e);
+    if (in->z.ptr) set_rows(k, bimamba::kGlrZ, in->z, e);
 }
 
 int check_workspace(const void* ws, size_t have, size_t need) {
@@ -128,17 +134,27 @@ int make_sync(bimamba::GlrSync& y, int batch, int D, int64_t tiles, unsigned fla
     return cudaMemsetAsync(ws, 0xff, sync_bytes(batch, D, tiles), st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
 }
 
-// Rows whose every start is aligned to `n` elements.
-bool starts_at(const GlrRows& q, size_t esz, int n) {
-    return !q.p || (aligned(q.p, n * esz) && q.bs % n == 0 && q.ts % n == 0);
+// Every row of the tensors from first to last starts at a multiple of `bytes`.
+bool starts_at(const GlrParams& k, int first, int last, int bytes) {
+    for (int q = first; q <= last; ++q) {
+        const GlrRows& r = k.rows[q];
+        if (r.p && (!aligned(r.p, bytes) || r.bs % bytes || r.ts % bytes)) return false;
+    }
+    return true;
 }
 
-// Bytes of one asynchronous copy that all rows read allow: 16, a pair, or 0 (single elements).
-template <typename... R>
-int copy_bytes(int D, size_t esz, R... q) {
-    const int wide = (int)(16 / esz);
-    if (D % wide == 0 && (starts_at(q, esz, wide) && ...)) return 16;
-    return D % 2 == 0 && (starts_at(q, esz, 2) && ...) ? (int)(2 * esz) : 0;
+// Bytes of one asynchronous copy that the inputs allow: 16, a pair, or 0 (single elements).
+int copy_bytes(const GlrParams& k, int esz) {
+    if (k.D * (int64_t)esz % 16 == 0 && starts_at(k, bimamba::kGlrR, bimamba::kGlrZ, 16)) return 16;
+    return k.D % 2 == 0 && starts_at(k, bimamba::kGlrR, bimamba::kGlrZ, 2 * esz) ? 2 * esz : 0;
+}
+
+// Outputs, and all fp32 vectors, in pairs.
+bool pairs(const GlrParams& k, int esz) {
+    for (const void* v : {(const void*)k.A, (const void*)k.r_bias, (const void*)k.i_bias, (const void*)k.h_in,
+                          (const void*)k.h_out, (const void*)k.chunk, (const void*)k.dh_out, (const void*)k.dh_in})
+        if (!aligned(v, 8)) return false;
+    return k.D % 2 == 0 && starts_at(k, bimamba::kGlrOut, bimamba::kGlrDz, 2 * esz);
 }
 
 // Blocks that stay: what the SMs hold at 128 registers a thread.
@@ -153,31 +169,48 @@ int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, in
     y.total = (unsigned)total;
     const size_t smem = warps * warp_bytes;
     if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), bimamba::kGlrWarps * warp_bytes))) return rc;
-    const int by_regs = 16 / warps, by_smem = (int)(227 * 1024 / (smem + 12 * 1024));
+    constexpr size_t kFixed = 17 * 1024 + 1024;  // static shared memory and the 1 KB that the system keeps
+    const int by_regs = 16 / warps, by_smem = (int)(228 * 1024 / (smem + kFixed));
     const int64_t held = (int64_t)kSms * std::max(1, std::min(by_regs, by_smem));
     fn<<<(unsigned)std::min(total, held), warps * 32, smem, st>>>(k, y);
     return launch_status();
 }
 
-template <typename T, bool VEC>
-int launch_fwd(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+template <typename T, bool VEC, int EPI>
+int launch_fwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
     const int64_t tiles = (k.L + TILE - 1) / TILE;
     const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
-    if (k.add.p || k.z.p)
-        return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, true>, k, tiles, warps,
-                            bimamba::kGlrFwdWarpBytes<T, true>, flags, ws, st);
-    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, false>, k, tiles, warps,
-                        bimamba::kGlrFwdWarpBytes<T, false>, flags, ws, st);
+    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI>, k, tiles, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
+                        flags, ws, st);
 }
 
-template <typename T, bool VEC>
-int launch_bwd(const GlrParams& k, unsigned flags, void* sync, cudaStream_t st) {
-    if (k.add.p || k.z.p)
-        return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, true>, k, k.nchunk, bimamba::kGlrWarps,
-                            bimamba::kGlrBwdWarpBytes<T, true>, flags, sync, st);
-    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, false>, k, k.nchunk, bimamba::kGlrWarps,
-                        bimamba::kGlrBwdWarpBytes<T, false>, flags, sync, st);
+template <typename T, bool VEC, int EPI>
+int launch_bwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI>, k, k.nchunk, bimamba::kGlrWarps,
+                        bimamba::kGlrBwdWarpBytes<T, EPI>, flags, ws, st);
+}
+
+template <bool BWD, typename T, bool VEC>
+int launch_vec(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+    const int epi = k.rows[bimamba::kGlrZ].p ? 2 : (k.rows[bimamba::kGlrAdd].p ? 1 : 0);
+    if constexpr (BWD) {
+        if (epi == 2) return launch_bwd_epi<T, VEC, 2>(k, flags, ws, st);
+        return epi ? launch_bwd_epi<T, VEC, 1>(k, flags, ws, st) : launch_bwd_epi<T, VEC, 0>(k, flags, ws, st);
+    } else {
+        if (epi == 2) return launch_fwd_epi<T, VEC, 2>(k, flags, ws, st);
+        return epi ? launch_fwd_epi<T, VEC, 1>(k, flags, ws, st) : launch_fwd_epi<T, VEC, 0>(k, flags, ws, st);
+    }
+}
+
+template <bool BWD>
+int launch(GlrParams& k, bimamba_dtype_t dtype, unsigned flags, void* ws, cudaStream_t st) {
+    const int e = (int)elem_size(dtype);
+    k.copy = copy_bytes(k, e);
+    const bool vec = pairs(k, e);
+    if (dtype == BIMAMBA_BF16)
+        return vec ? launch_vec<BWD, bf16, true>(k, flags, ws, st) : launch_vec<BWD, bf16, false>(k, flags, ws, st);
+    return vec ? launch_vec<BWD, float, true>(k, flags, ws, st) : launch_vec<BWD, float, false>(k, flags, ws, st);
 }
 
 // The backward's partial sums, one row of 3 D per chunk, in whole 256 bytes.
@@ -208,17 +241,11 @@ int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
 
     GlrParams k = {};
     fill_common(k, in, p, batch, L, d_inner, flags);
-    k.out = rows(*out);
+    set_rows(k, bimamba::kGlrOut, *out, elem_size(in->dtype));
     k.h_in = h_in;
     k.h_out = h_out;
     k.chunk = chunk_states;
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    const size_t e = elem_size(in->dtype);
-    k.copy = copy_bytes(d_inner, e, k.x, k.r, k.i, k.add, k.z);
-    const bool vec = d_inner % 2 == 0 && starts_at(k.out, e, 2);
-    if (in->dtype == BIMAMBA_BF16)
-        return vec ? launch_fwd<bf16, true>(k, flags, workspace, st) : launch_fwd<bf16, false>(k, flags, workspace, st);
-    return vec ? launch_fwd<float, true>(k, flags, workspace, st) : launch_fwd<float, false>(k, flags, workspace, st);
+    return launch<false>(k, in->dtype, flags, workspace, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* p, const bimamba_rows_t* dout,
@@ -229,7 +256,7 @@ int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     if (rc) return rc;
     if (!dout || !chunk_states || !grads) return BIMAMBA_ERR_INVALID_ARG;
     const size_t e = elem_size(in->dtype);
-    if ((rc = check_in(*dout, e, false))) return rc;
+    if ((rc = check_in(*dout, e, L, false))) return rc;
     if ((rc = check_out(grads->dx, e, batch, L, d_inner))) return rc;
     if ((rc = check_out(grads->dr, e, batch, L, d_inner))) return rc;
     if ((rc = check_out(grads->di, e, batch, L, d_inner))) return rc;
@@ -242,25 +269,19 @@ int bimamba_glr_bwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
 
     GlrParams k = {};
     fill_common(k, in, p, batch, L, d_inner, flags);
-    k.dout = rows(*dout);
-    k.dx = rows(grads->dx);
-    k.dr = rows(grads->dr);
-    k.di = rows(grads->di);
-    k.dadd = rows(grads->dadd);
-    k.dz = rows(grads->dz);
+    set_rows(k, bimamba::kGlrDout, *dout, e);
+    set_rows(k, bimamba::kGlrDx, grads->dx, e);
+    set_rows(k, bimamba::kGlrDr, grads->dr, e);
+    set_rows(k, bimamba::kGlrDi, grads->di, e);
+    if (in->add.ptr) set_rows(k, bimamba::kGlrDadd, grads->dadd, e);
+    if (in->z.ptr) set_rows(k, bimamba::kGlrDz, grads->dz, e);
     k.chunk = const_cast<float*>(chunk_states);
     k.dh_out = dh_out;
     k.dh_in = grads->dh_in;
     k.part = static_cast<float*>(workspace);
     unsigned char* sync = static_cast<unsigned char*>(workspace) + part_bytes(batch, L, d_inner);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    k.copy = copy_bytes(d_inner, e, k.x, k.r, k.i, k.dout, k.add, k.z);
-    const bool vec = d_inner % 2 == 0 && starts_at(k.dx, e, 2) && starts_at(k.dr, e, 2) && starts_at(k.di, e, 2) &&
-                     (!k.add.p || starts_at(k.dadd, e, 2)) && (!k.z.p || starts_at(k.dz, e, 2));
-    if (in->dtype == BIMAMBA_BF16)
-        rc = vec ? launch_bwd<bf16, true>(k, flags, sync, st) : launch_bwd<bf16, false>(k, flags, sync, st);
-    else
-        rc = vec ? launch_bwd<float, true>(k, flags, sync, st) : launch_bwd<float, false>(k, flags, sync, st);
+    rc = launch<true>(k, in->dtype, flags, sync, st);
     if (rc || !(grads->dA || grads->dr_bias || grads->di_bias)) return rc;
     bimamba::glr_sums_kernel<<<(unsigned)((3LL * d_inner + 31) / 32), 1024, 0, st>>>(
         k.part, batch * k.nchunk, d_inner, grads->dA, grads->dr_bias, grads->di_bias);

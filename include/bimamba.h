@@ -443,6 +443,10 @@ int bimamba_out_proj(const void *y, const void *w_out, int batch, int64_t L, int
 /* Tokens between the states that a forward call saves for the backward. */
 #define BIMAMBA_GLR_CHUNK 64
 
+/* The longest token stride of a tensor of more than one token, in elements
+ * (a longer one is UNSUPPORTED). */
+#define BIMAMBA_GLR_MAX_TOKEN_STRIDE 0x1fffffff
+
 /* Token rows of d_inner elements: element (b, t, d) is at
  * ptr[b * batch_stride + t * token_stride + d] (strides in elements, >= 0). */
 typedef struct {
