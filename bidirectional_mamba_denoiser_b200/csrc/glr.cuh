@@ -238,9 +238,11 @@ constexpr unsigned kGlrErrTimeout = 4u;  // a wait for an earlier tile gave up
 
 static __device__ unsigned int g_glr_error;
 
+constexpr int kGlrGone = 32;  // a line of its own
+
 struct GlrSync {
-    unsigned int* ticket;        // [0] the tickets, [1] set once a wait ran out; all ones before the launch.
-                                 // Null: one tile a row, nothing to hand over
+    unsigned int* ticket;        // [0] the tickets, [kGlrGone] zero once a wait ran out; all ones before the
+                                 // launch.  Null: one tile a row, nothing to hand over
     unsigned long long* map;     // [batch * slabs][tiles][64]: (P, h) of each channel
     float* state;                // [batch * slabs][groups][64]: state entering each group
     int64_t tiles, groups;
@@ -321,13 +323,14 @@ __device__ __forceinline__ void glr_ask(GlrPiece& q, const GlrSync& y, const Glr
 __device__ __forceinline__ float4 glr_wait_piece(const GlrSync& y, GlrPiece q, const GlrTile& t, int warp) {
     if ((unsigned)q.v[0] == 0xffffffffu || (unsigned)q.v[1] == 0xffffffffu) {
         const long long t0 = clock64();
-        for (;;) {
+        for (int tries = 1;; ++tries) {
             glr_ask(q, y, t, warp);
             if ((unsigned)q.v[0] != 0xffffffffu && (unsigned)q.v[1] != 0xffffffffu) break;
+            if (tries % 64) continue;  // the word that all waits share is looked at rarely
             unsigned gone;
-            asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(gone) : "l"(y.ticket + 1) : "memory");
+            asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(gone) : "l"(y.ticket + kGlrGone) : "memory");
             if (gone == 0u || clock64() - t0 > y.wait_limit) {
-                atomicExch(y.ticket + 1, 0u);
+                atomicExch(y.ticket + kGlrGone, 0u);
                 atomicOr(&g_glr_error, kGlrErrTimeout);
                 q.v[0] = q.v[1] = 0;
                 break;
@@ -344,6 +347,17 @@ __device__ __forceinline__ float2 glr_apply(float4 q, float2 c) {
     return glr_fma(make_float2(q.x, q.z), c, make_float2(q.y, q.w));
 }
 
+// c through the first n (at most 7) maps (all read at once).
+__device__ __forceinline__ float2 glr_through(const float4 (*maps)[32], float2 c, int n) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 0; w < 7; ++w) {
+        const float4 q = maps[w][lane];
+        if (w < n) c = glr_apply(q, c);
+    }
+    return c;
+}
+
 // The tile's first step.  BWD: tiles are walked from the row's last to its
 // first, then those past its length.
 template <bool BWD>
@@ -353,13 +367,15 @@ __device__ __forceinline__ int64_t glr_first_step(const GlrTile& t, int tile_ste
     return (t.at < used ? used - 1 - t.at : t.at) * tile_steps;
 }
 
-// The tiles of a block, in shared memory, a few ahead, each with the address
-// of its first step in every tensor.  Warp 0 looks them up (each lane one
-// tensor's address) and takes a ticket a turn before it is looked up.
+// The tiles of a block, in shared memory, a few ahead, each with the byte
+// offset of its first step in every tensor (an offset: of an address out of
+// shared memory the compiler would not know that it is global).  Warp 0 looks
+// them up (each lane one tensor's offset) and takes a ticket a turn before it
+// is looked up.
 constexpr int kGlrQueue = 4;
 struct GlrEntry {
     GlrTile t;
-    char* at[kGlrTensors];
+    int64_t off[kGlrTensors];
 };
 template <bool BWD, int ESZ>
 struct GlrQueue {
@@ -382,7 +398,7 @@ struct GlrQueue {
             const int64_t s = glr_first_step<BWD>(t, tile_steps);
             // in reverse the token of step s is len - 1 - s, and ts < 0
             const int64_t off = p.reverse ? (s - (t.len - 1)) * r.ts : s * r.ts;
-            e.at[threadIdx.x] = r.p + t.b * r.bs + off + (int64_t)glr_channel(p, t) * ESZ;
+            e.off[threadIdx.x] = t.b * r.bs + off + (int64_t)glr_channel(p, t) * ESZ;
         }
     }
     __device__ __forceinline__ void start(const GlrParams& p, const GlrSync& y, int n) {
@@ -415,7 +431,7 @@ template <typename T, int TOK>
 __device__ __forceinline__ void glr_copy_rows(T* to, const GlrParams& p, const GlrEntry& e, int tensor, int first, int n,
                                               int left) {
     const int lane = threadIdx.x & 31;
-    const char* const tile = e.at[tensor];
+    const char* const tile = p.rows[tensor].p + e.off[tensor];
     const int64_t ts = p.rows[tensor].ts;
     if (p.copy == 16) {
         constexpr int E = 16 / sizeof(T), PER = kGlrSlab / E, ROWS = 32 / PER;  // elements a copy, copies a row
@@ -584,8 +600,10 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const bool last = s1 >= t.len, publish = y.ticket && !last && !y.starve;
         float2 P = glr_f2(1.f), h = glr_f2(0.f);
         if (warp == 0) {
-            for (int w = 0; w < nwarp; ++w) {
+#pragma unroll
+            for (int w = 0; w < kGlrWarps; ++w) {
                 const float4 q = agg[w][lane];
+                if (w >= nwarp) continue;
                 P = glr_mul(P, make_float2(q.x, q.z));
                 h = glr_apply(q, h);
             }
@@ -597,7 +615,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         const float4 from = got[kGlrGroup - 1][lane];
         float2 c = make_float2(from.y, from.w);
-        for (int w = 0; w < t.at % kGlrGroup; ++w) c = glr_apply(got[w][lane], c);
+        c = glr_through(got, c, t.at % kGlrGroup);
         if (warp == 0) {
             const float2 end = glr_fma(P, c, h);
             // the other tiles take a row's first state from here, not from h_in, which may be h_out
@@ -606,7 +624,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                 glr_publish_state(glr_state(y, t, t.at + 1), end);
             if (last && p.h_out) glr_st2<VEC>(p.h_out + row, end, nch);
         }
-        for (int w = 0; w < warp; ++w) c = glr_apply(agg[w][lane], c);
+        c = glr_through(agg, c, warp);
         copy_inputs(queue[(k + NS) % kGlrQueue], stage);
         if (p.chunk && n > 0 && ws % kGlrChunk == 0)
             glr_st2<VEC>(p.chunk + ((int64_t)t.b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
@@ -615,7 +633,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             __syncwarp();
         }
         const int64_t ts = p.rows[kGlrOut].ts;
-        char* po = e.at[kGlrOut] + warp * TOK * ts + 2 * lane * (int)sizeof(T);
+        char* po = p.rows[kGlrOut].p + e.off[kGlrOut] + warp * TOK * ts + 2 * lane * (int)sizeof(T);
         auto outputs = [&](auto full) {
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
@@ -767,8 +785,10 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             const bool last = s0 == 0, publish = y.ticket && !last && !y.starve;
             // the map from the tile's end to the warp's, and for warp 0 to the tile's start
             float2 Pw = glr_f2(1.f), qw = glr_f2(0.f);
-            for (int w = kGlrWarps - 1; w > warp; --w) {
+#pragma unroll
+            for (int w = kGlrWarps - 1; w > 0; --w) {
                 const float4 a = agg[w][lane];
+                if (w <= warp) continue;
                 Pw = glr_mul(Pw, make_float2(a.x, a.z));
                 qw = glr_apply(a, qw);
             }
@@ -786,9 +806,11 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             // the states before the warp's steps, from the one that enters the tile
             if (n) {
                 float2 c = entering;
-                for (int w = 0; w < warp; ++w) {
+#pragma unroll
+                for (int w = 0; w < kGlrWarps - 1; ++w) {
                     const float4 a = agg[w][lane];
-                    c = glr_fma(make_float2(a.x, a.z), c, aggh[w][lane]);
+                    const float2 hw = aggh[w][lane];
+                    if (w < warp) c = glr_fma(make_float2(a.x, a.z), c, hw);
                 }
 #pragma unroll
                 for (int j = 0; j < TOK; ++j) {
@@ -799,7 +821,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             __syncthreads();
             const float4 from = pieces[kGlrGroup - 1][lane];
             float2 c = make_float2(from.y, from.w);
-            for (int w = 0; w < t.at % kGlrGroup; ++w) c = glr_apply(pieces[w][lane], c);
+            c = glr_through(pieces, c, t.at % kGlrGroup);
             if (warp == 0) {
                 const float2 end = glr_fma(P, c, q);
                 // the other tiles take the last state's gradient from here, not from dh_out, which may be dh_in
@@ -810,10 +832,14 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             }
             q = glr_fma(Pw, c, qw);
             const float2 A = glr_vec2<VEC>(p.A, c0, nch);
-            const int col = 2 * lane * (int)sizeof(T);
-            auto to = [&](int tensor, int j) {
-                const int64_t ts = p.rows[tensor].ts;
-                return reinterpret_cast<T*>(e.at[tensor] + (warp * TOK + j) * ts + col);
+            // where the warp's steps go, from its last to its first
+            char* to[kGlrDz - kGlrDx + 1];
+#pragma unroll
+            for (int k = kGlrDx; k <= kGlrDz; ++k)
+                to[k - kGlrDx] = p.rows[k].p + e.off[k] + (int64_t)p.rows[k].ts * (warp * TOK + TOK - 1) +
+                                 2 * lane * (int)sizeof(T);
+            auto put = [&](int tensor, int j, float2 v) {
+                glr_st2<VEC>(reinterpret_cast<T*>(to[tensor - kGlrDx] - (TOK - 1 - j) * (int64_t)p.rows[tensor].ts), v, nch);
             };
             auto outputs = [&](auto full) {
 #pragma unroll
@@ -829,19 +855,19 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                         const float2 h = glr_add(glr_fma(a, hp[j], w), glr_row(in_add, j));
                         // silu'(z) = s (1 + z (1 - s))
                         const float2 ds = glr_mul(sz, glr_fma(z, glr_one_minus(sz), 1.f));
-                        glr_st2<VEC>(to(kGlrDz, j), glr_mul(glr_mul(dh, h), ds), nch);
+                        put(kGlrDz, j, glr_mul(glr_mul(dh, h), ds));
                         dh = glr_mul(dh, glr_mul(z, sz));
                     }
-                    if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) glr_st2<VEC>(to(kGlrDadd, j), dh, nch);
+                    if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);
                     const float2 G = glr_add(dh, q);
                     q = glr_mul(a, G);
                     const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
                     const float2 dla = glr_mul(G, glr_sub(glr_mul(a, hp[j]), glr_mul(glr_mul(ab, ab), w)));
                     const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_one_minus(rg[j])));
                     const float2 di = glr_mul(glr_mul(G, w), glr_one_minus(ig[j]));
-                    glr_st2<VEC>(to(kGlrDx, j), glr_mul(G, bi), nch);
-                    glr_st2<VEC>(to(kGlrDr, j), dr, nch);
-                    glr_st2<VEC>(to(kGlrDi, j), di, nch);
+                    put(kGlrDx, j, glr_mul(G, bi));
+                    put(kGlrDr, j, dr);
+                    put(kGlrDi, j, di);
                     sA = glr_fma(rg[j], dla, sA);
                     sr = glr_add(sr, dr);
                     si = glr_add(si, di);
