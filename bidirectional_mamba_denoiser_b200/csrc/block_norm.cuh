@@ -17,10 +17,18 @@
 // never a difference of large sums), and the backward's column sums stay in
 // registers over all rows of a block.  Row sums are fp32, through warp
 // shuffles and, for rows wider than a warp, shared memory.
+//
+// Two forms.  Rows of 256 to 8192 columns in whole groups of eight: a block
+// walks a run of one batch row's tokens, every thread copying its own columns
+// of the rows ahead into shared memory (cp.async; a thread reads back only what
+// it copied, so no barrier), with the vectors in registers for the whole run.
+// Other rows: a warp or a block a row, straight from memory.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <stdint.h>
+
+#include "tma_util.cuh"
 
 namespace bimamba {
 
@@ -46,7 +54,7 @@ struct BlockNormParams {
     int batch, d;
     int gate_bs, gamma_bs;  // floats between batch rows: d, or 0 when shared
     int rms;
-    int nseg;               // backward: row segments per batch row
+    int nseg;               // row segments per batch row (backward, and the copying form)
 };
 
 // V neighbouring elements <-> fp32 (V = 8: 16- or 32-byte rows of a 16-byte
@@ -335,18 +343,367 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_kernel(const
     }
 }
 
-// The column sums over the partial rows, in row order: of one batch row
-// (blockIdx.z), or of all for the shared vectors.  blockIdx.y: which vector.
-__global__ void block_norm_sums_kernel(const float* part, int nseg, int batch, int d, float* dgate, float* dpost_w,
-                                       float* dgamma, float* dbeta, int gate_shared, int gamma_shared) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, which = blockIdx.y;
+// ---------------------------------------------------------------- rows copied ahead
+
+// The sums of v over the block, one barrier for the pair (`red`: two buffers in turn).
+__device__ __forceinline__ float2 bn_block_sum2(float2 v, float2 (*red)[32], int& turn) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    }
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    float2* r = red[turn];
+    turn ^= 1;
+    if (lane == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) {  // at most 16 warps, in both halves
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    }
+    return v;
+}
+__device__ __forceinline__ float bn_block_sum(float v, float2 (*red)[32], int& turn) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    float2* r = red[turn];
+    turn ^= 1;
+    if (lane == 0) r[threadIdx.x >> 5].x = v;
+    __syncthreads();
+    v = (lane & 15) < nw ? r[lane & 15].x : 0.f;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// 16-byte pieces of eight elements.
+template <typename T>
+constexpr int kBnPieces = (int)sizeof(T) / 2;
+
+// A thread's eight columns of a row into its pieces of a stage, and back.
+// Piece q of thread t is at stage + (q * blockDim.x + t) * 16.
+template <typename T>
+__device__ __forceinline__ void bn_fetch(unsigned char* stage, int q, const T* row) {
+#pragma unroll
+    for (int h = 0; h < kBnPieces<T>; ++h)
+        cp_async<16>(stage + ((q + h) * blockDim.x + threadIdx.x) * 16, reinterpret_cast<const char*>(row) + 16 * h, true);
+}
+template <typename T>
+__device__ __forceinline__ void bn_fetched(const unsigned char* stage, int q, float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        bn_load<8>(reinterpret_cast<const __nv_bfloat16*>(stage + (q * blockDim.x + threadIdx.x) * 16), v);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 a = *reinterpret_cast<const float4*>(stage + ((q + h) * blockDim.x + threadIdx.x) * 16);
+            v[4 * h] = a.x, v[4 * h + 1] = a.y, v[4 * h + 2] = a.z, v[4 * h + 3] = a.w;
+        }
+    }
+}
+
+// Vectors of a thread's columns: held in registers for one group of columns,
+// read again a row (they stay in L1) for two.
+template <int K, bool HOLD>
+struct BnVec {
+    const float* p;
+    float other;
+    float v[HOLD ? K : 1][8];
+    __device__ __forceinline__ void start(const float* q, float without, int col0, int step, int d) {
+        p = q;
+        other = without;
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (col0 + k * step < d) bn_vec<8>(p, col0 + k * step, other, v[k]);
+        }
+    }
+    __device__ __forceinline__ void get(int k, int c, float (&o)[8]) const {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = v[k][e];
+        } else {
+            bn_vec<8>(p, c, other, o);
+        }
+    }
+};
+
+template <int K>
+constexpr int kBnStages = K == 1 ? 4 : 2;
+template <typename TS, typename TU, int K>
+constexpr int kBnFwdPieces = K * (kBnPieces<TS> + kBnPieces<TU>);
+template <typename TS, typename TU, int K>
+constexpr int kBnBwdPieces = K * 2 * (kBnPieces<TS> + kBnPieces<TU>);
+
+template <typename TS, typename TU, int K>
+__global__ void __launch_bounds__(kBlockNormThreads, K == 1 ? 2 : 1) block_norm_fwd_run_kernel(const BlockNormParams p) {
+    constexpr int NS = kBnStages<K>, PIECES = kBnFwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
+    extern __shared__ __align__(16) unsigned char bn_smem[];
+    __shared__ float2 red[2][32];
+    int turn = 0;
+    const int64_t b = blockIdx.y;
+    const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    const int64_t r0 = b * p.L + p.L * seg / p.nseg, r1 = b * p.L + p.L * (seg + 1) / p.nseg;
+    auto fetch = [&](int64_t row, int s) {
+        if (row < r1) {
+            unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                if (c >= d) continue;
+                bn_fetch(stage, k * (PS + PU), static_cast<const TS*>(p.x) + row * d + c);
+                if (p.u) bn_fetch(stage, k * (PS + PU) + PS, static_cast<const TU*>(p.u) + row * d + c);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) fetch(r0 + s, s);
+    BnVec<K, K == 1> gate, post_w, gamma, beta;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
+    post_w.start(p.post_w, 1.f, col0, step, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
+    beta.start(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, col0, step, d);
+    const float per = 1.f / (float)d;
+    // mean (0 with rms) and 1/sigma of the row held in v
+    auto stats = [&](const float (&v)[K][8], float& mu, float& rs) {
+        mu = 0.f;
+        if (!p.rms) {
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += v[k][e];  // columns past d hold 0
+            mu = bn_block_sum(s, red, turn) * per;
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (col0 + k * step < d) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q = fmaf(v[k][e] - mu, v[k][e] - mu, q);
+            }
+        rs = rsqrtf(bn_block_sum(q, red, turn) * per + p.eps);
+    };
+    int s = 0;
+    for (int64_t row = r0; row < r1; ++row) {
+        const unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+        cp_async_wait_pending<NS - 1>();
+        float x[K][8], u[K][8];
+        float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = u[k][e] = 0.f;
+            if (col0 + k * step < d) {
+                bn_fetched<TS>(stage, k * (PS + PU), x[k]);
+                if (p.u) bn_fetched<TU>(stage, k * (PS + PU) + PS, u[k]);
+            }
+        }
+        fetch(row + NS, s);
+        s = s + 1 == NS ? 0 : s + 1;
+        if (p.post_w) stats(u, st.z, st.w);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = col0 + k * step;
+            if (c >= d) continue;
+            float g[8];
+            if (p.post_w) {
+                post_w.get(k, c, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[k][e] = (u[k][e] - st.z) * st.w * g[e];
+            }
+            gate.get(k, c, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = bn_round<TS>(fmaf(g[e], u[k][e], p.res_scale * x[k][e]));
+            if (p.x_out) bn_store<8>(static_cast<TS*>(p.x_out) + row * d + c, x[k]);
+        }
+        if (p.y) {
+            stats(x, st.x, st.y);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                if (c >= d) continue;
+                float g[8], be[8];
+                gamma.get(k, c, g);
+                beta.get(k, c, be);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = fmaf(g[e], (x[k][e] - st.x) * st.y, be[e]);
+                bn_store<8>(static_cast<TU*>(p.y) + row * d + c, x[k]);
+            }
+        }
+        if (p.stats && threadIdx.x == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
+    }
+    cp_async_wait_all();
+}
+
+template <typename TS, typename TU, int K>
+__global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(const BlockNormParams p) {
+    constexpr int NS = kBnStages<K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
+    extern __shared__ __align__(16) unsigned char bn_smem[];
+    __shared__ float2 red[2][32];
+    int turn = 0;
+    const int64_t b = blockIdx.y;
+    const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    const int64_t r0 = b * p.L + p.L * seg / p.nseg, r1 = b * p.L + p.L * (seg + 1) / p.nseg;
+    auto fetch = [&](int64_t row, int s) {
+        if (row < r1) {
+            unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step, q = k * 2 * (PS + PU);
+                if (c >= d) continue;
+                if (p.dy) {
+                    bn_fetch(stage, q, static_cast<const TS*>(p.x) + row * d + c);
+                    bn_fetch(stage, q + PS, static_cast<const TU*>(p.dy) + row * d + c);
+                }
+                if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + row * d + c);
+                if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + row * d + c);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) fetch(r0 + s, s);
+    BnVec<K, K == 1> gate, post_w, gamma;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
+    post_w.start(p.post_w, 1.f, col0, step, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
+    const float per = 1.f / (float)d;
+    float sg[K][8], sw[K][8], sm[K][8], sb[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sg[k][e] = sw[k][e] = sm[k][e] = sb[k][e] = 0.f;
+    int s = 0;
+    for (int64_t row = r0; row < r1; ++row) {
+        const unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+        const float4 st = reinterpret_cast<const float4*>(p.stats)[row];
+        cp_async_wait_pending<NS - 1>();
+        float n[K][8], dy[K][8], D[K][8];
+        float2 sum = make_float2(0.f, 0.f);
+        if (p.dy) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step, q = k * 2 * (PS + PU);
+                if (c >= d) continue;
+                bn_fetched<TS>(stage, q, n[k]);
+                bn_fetched<TU>(stage, q + PS, dy[k]);
+                float ga[8];
+                gamma.get(k, c, ga);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    n[k][e] = (n[k][e] - st.x) * st.y;
+                    sm[k][e] = fmaf(dy[k][e], n[k][e], sm[k][e]);
+                    sb[k][e] += dy[k][e];
+                    dy[k][e] *= ga[e];
+                    sum.x += dy[k][e];
+                    sum.y = fmaf(dy[k][e], n[k][e], sum.y);
+                }
+            }
+            sum = bn_block_sum2(sum, red, turn);
+            sum = make_float2(p.rms ? 0.f : sum.x * per, sum.y * per);
+        }
+        float2 tu = make_float2(0.f, 0.f);
+        float u[K][8];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = col0 + k * step, q = k * 2 * (PS + PU);
+            if (c >= d) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) D[k][e] = 0.f;
+            if (p.dx_out) bn_fetched<TS>(stage, q + PS + PU, D[k]);
+            if (p.u) bn_fetched<TU>(stage, q + 2 * PS + PU, u[k]);
+            if (p.dy) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) D[k][e] = fmaf(st.y, dy[k][e] - fmaf(n[k][e], sum.y, sum.x), D[k][e]);
+            }
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = p.res_scale * D[k][e];
+            bn_store<8>(static_cast<TS*>(p.dx) + row * d + c, o);
+            if (!p.u) continue;
+            float ga[8], w[8];
+            gate.get(k, c, ga);
+            if (p.post_w) {
+                post_w.get(k, c, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float m = (u[k][e] - st.z) * st.w, g = ga[e] * D[k][e], gw = g * w[e];
+                    sg[k][e] = fmaf(D[k][e], m * w[e], sg[k][e]);
+                    sw[k][e] = fmaf(g, m, sw[k][e]);
+                    tu.x += gw;
+                    tu.y = fmaf(gw, m, tu.y);
+                    u[k][e] = m;
+                    D[k][e] = gw;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sg[k][e] = fmaf(D[k][e], u[k][e], sg[k][e]);
+                    o[e] = ga[e] * D[k][e];
+                }
+                bn_store<8>(static_cast<TU*>(p.du) + row * d + c, o);
+            }
+        }
+        fetch(row + NS, s);
+        s = s + 1 == NS ? 0 : s + 1;
+        if (p.u && p.post_w) {
+            tu = bn_block_sum2(tu, red, turn);
+            tu = make_float2(p.rms ? 0.f : tu.x * per, tu.y * per);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                if (c >= d) continue;
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = st.w * (D[k][e] - fmaf(u[k][e], tu.y, tu.x));
+                bn_store<8>(static_cast<TU*>(p.du) + row * d + c, o);
+            }
+        }
+    }
+    cp_async_wait_all();
+    if (!p.part) return;
+    float* q = p.part + ((int64_t)b * p.nseg + seg) * 4 * d;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = col0 + k * step;
+        if (c >= d) continue;
+        bn_store<8>(q + c, sg[k]);
+        bn_store<8>(q + d + c, sw[k]);
+        bn_store<8>(q + 2 * (int64_t)d + c, sm[k]);
+        bn_store<8>(q + 3 * (int64_t)d + c, sb[k]);
+    }
+}
+
+// The column sums over the partial rows: of one batch row (blockIdx.z), or
+// of all for the shared vectors.  blockIdx.y: which vector.  A block takes 32
+// columns, each of its warps every sixteenth row; their sums are added in order.
+constexpr int kBnSumWarps = 16;
+__global__ void __launch_bounds__(kBnSumWarps * 32)
+    block_norm_sums_kernel(const float* part, int nseg, int batch, int d, float* dgate, float* dpost_w, float* dgamma,
+                           float* dbeta, int gate_shared, int gamma_shared) {
+    __shared__ float sum[kBnSumWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, which = blockIdx.y;
     float* out = which == 0 ? dgate : which == 1 ? dpost_w : which == 2 ? dgamma : dbeta;
     const bool shared = which == 1 || (which == 0 ? gate_shared : gamma_shared);
     const int64_t b = blockIdx.z;
-    if (c >= d || !out || (shared && b > 0)) return;
+    if (!out || (shared && b > 0)) return;
     const int64_t k0 = shared ? 0 : b * nseg, k1 = shared ? (int64_t)batch * nseg : k0 + nseg;
     float s = 0.f;
-    for (int64_t k = k0; k < k1; ++k) s += part[(k * 4 + which) * d + c];
+    if (c < d) {
+#pragma unroll 4
+        for (int64_t k = k0 + warp; k < k1; k += kBnSumWarps) s += part[(k * 4 + which) * d + c];
+    }
+    sum[warp][lane] = s;
+    __syncthreads();
+    if (warp || c >= d) return;
+    s = 0.f;
+    for (int w = 0; w < kBnSumWarps; ++w) s += sum[w][lane];
     out[(shared ? 0 : b * d) + c] = s;
 }
 

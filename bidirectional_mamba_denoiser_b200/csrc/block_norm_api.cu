@@ -90,16 +90,65 @@ int launch_shape(const BlockNormParams& k, const Shape& s, cudaStream_t st) {
 }
 
 template <bool BWD>
-int launch(const BlockNormParams& k, const Shape& s, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
+int launch_rows(const BlockNormParams& k, const Shape& s, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
     if (ts == BIMAMBA_BF16) return launch_shape<BWD, bf16, bf16>(k, s, st);
     if (tu == BIMAMBA_BF16) return launch_shape<BWD, float, bf16>(k, s, st);
     return launch_shape<BWD, float, float>(k, s, st);
 }
 
+constexpr size_t kMaxRunSmem = 200 * 1024;
+
+// The copying form: 32 to 512 threads of K = 1 or 2 groups of eight columns.
+// False where the copies ahead would not fit (two stages of wide fp32 rows).
+template <bool BWD, typename TS, typename TU, int K>
+bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
+    constexpr int pieces = BWD ? bimamba::kBnBwdPieces<TS, TU, K> : bimamba::kBnFwdPieces<TS, TU, K>;
+    const int threads = ((k.d / 8 + K - 1) / K + 31) / 32 * 32;
+    const size_t smem = (size_t)bimamba::kBnStages<K> * pieces * threads * 16;
+    if (smem > kMaxRunSmem) return false;
+    void (*fn)(BlockNormParams);
+    if constexpr (BWD)
+        fn = bimamba::block_norm_bwd_run_kernel<TS, TU, K>;
+    else
+        fn = bimamba::block_norm_fwd_run_kernel<TS, TU, K>;
+    // one limit for all widths: it is raised once a kernel
+    if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), kMaxRunSmem))) return true;
+    if (!BWD) {  // one run a block that an SM holds (64 registers a thread, 128 for K = 2)
+        const int held = (int)std::min<size_t>(std::min(1024 / K / threads, 16), 220 * 1024 / (smem + 2048));
+        k.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(k.L, (int64_t)kSms * std::max(held, 1) / k.batch));
+    }
+    fn<<<dim3((unsigned)k.nseg, (unsigned)k.batch), threads, smem, st>>>(k);
+    rc = launch_status();
+    return true;
+}
+
+template <bool BWD, typename TS, typename TU>
+bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
+    return k.d <= 8 * bimamba::kBlockNormThreads ? launch_run_k<BWD, TS, TU, 1>(k, st, rc)
+                                                 : launch_run_k<BWD, TS, TU, 2>(k, st, rc);
+}
+
+template <bool BWD>
+int launch(BlockNormParams& k, bool vec, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
+    if (vec && k.d >= 256 && k.d <= 16 * bimamba::kBlockNormThreads) {  // narrower rows would not fill a warp
+        int rc = BIMAMBA_OK;
+        if (ts == BIMAMBA_BF16 ? launch_run<BWD, bf16, bf16>(k, st, rc)
+                               : (tu == BIMAMBA_BF16 ? launch_run<BWD, float, bf16>(k, st, rc)
+                                                     : launch_run<BWD, float, float>(k, st, rc)))
+            return rc;
+    }
+    return launch_rows<BWD>(k, shape_for(k.d, vec), ts, tu, st);
+}
+
 // Row segments of the backward per batch row, each with its own column sums:
-// about four blocks an SM in all, and at least 8 rows a segment.
-int segments(int batch, int64_t L) {
-    const int64_t want = std::max<int64_t>(1, 4 * 148 / batch), most = std::max<int64_t>(1, L / 8);
+// one for each block (128 registers a thread) or warp that the SMs hold, but at
+// least 8 rows a segment.
+int segments(int batch, int64_t L, int d) {
+    const bool copying = d % 8 == 0 && d >= 256;
+    const int groups = d % 8 ? d : d / 8;
+    const int held = copying ? std::max(1, std::min(16, 512 / std::min(512, (groups + 31) / 32 * 32)))
+                             : (groups <= 128 ? 16 : 1);
+    const int64_t want = std::max<int64_t>(1, (int64_t)held * kSms / batch), most = std::max<int64_t>(1, L / 8);
     return (int)std::min(want, most);
 }
 
@@ -132,14 +181,13 @@ int bimamba_block_norm_fwd(const void* x, const void* u, const bimamba_block_nor
     k.x_out = x_out;
     k.y = y;
     k.stats = stats;
-    const bool vec = d % 8 == 0 && all_aligned16(x, u, x_out, y, (const void*)p->gate, (const void*)p->post_w,
-                                                 (const void*)p->gamma, (const void*)p->beta);
-    return launch<false>(k, shape_for(d, vec), stream_dtype, dtype, static_cast<cudaStream_t>(cuda_stream));
+    const bool vec = d % 8 == 0 && all_aligned16(x, u, x_out, y, stats, p->gate, p->post_w, p->gamma, p->beta);
+    return launch<false>(k, vec, stream_dtype, dtype, static_cast<cudaStream_t>(cuda_stream));
 }
 
 size_t bimamba_block_norm_workspace_bytes(int batch, int64_t L, int d) {
     if (!sizes_ok(batch, L, d)) return 0;
-    return (size_t)batch * segments(batch, L) * 4 * (size_t)d * sizeof(float);
+    return (size_t)batch * segments(batch, L, d) * 4 * (size_t)d * sizeof(float);
 }
 
 int bimamba_block_norm_bwd(const void* dy, const void* dx_out, const void* x_out, const void* u, const float* stats,
@@ -172,15 +220,15 @@ int bimamba_block_norm_bwd(const void* dy, const void* dx_out, const void* x_out
     k.dx_out = dx_out;
     k.dx = g->dx;
     k.du = g->du;
-    k.nseg = segments(batch, L);
+    k.nseg = segments(batch, L, d);
     const bool sums = g->dgate || g->dpost_w || g->dgamma || g->dbeta;
     k.part = sums ? static_cast<float*>(workspace) : nullptr;
-    const bool vec = d % 8 == 0 && all_aligned16(dy, dx_out, x_out, u, (const void*)g->dx, (const void*)g->du,
-                                                 (const void*)p->gate, (const void*)p->post_w, (const void*)p->gamma);
+    const bool vec = d % 8 == 0 && all_aligned16(dy, dx_out, x_out, u, (const void*)g->dx, (const void*)g->du, stats,
+                                                 p->gate, p->post_w, p->gamma);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    if ((rc = launch<true>(k, shape_for(d, vec), stream_dtype, dtype, st)) || !sums) return rc;
-    const dim3 grid((unsigned)((d + 127) / 128), 4, (unsigned)batch);
-    bimamba::block_norm_sums_kernel<<<grid, 128, 0, st>>>(
+    if ((rc = launch<true>(k, vec, stream_dtype, dtype, st)) || !sums) return rc;
+    const dim3 grid((unsigned)((d + 31) / 32), 4, (unsigned)batch);
+    bimamba::block_norm_sums_kernel<<<grid, 32 * bimamba::kBnSumWarps, 0, st>>>(
         k.part, k.nseg, batch, d, g->dgate, g->dpost_w, g->dgamma, g->dbeta, (flags & BIMAMBA_NORM_GATE_SHARED) != 0,
         (flags & BIMAMBA_NORM_GAMMA_SHARED) != 0);
     return launch_status();
