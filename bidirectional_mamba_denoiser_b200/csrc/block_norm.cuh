@@ -345,13 +345,62 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_kernel(const
 
 // ---------------------------------------------------------------- rows copied ahead
 
-// The sums of v over the block, one barrier for the pair (`red`: two buffers in turn).
-__device__ __forceinline__ float2 bn_block_sum2(float2 v, float2 (*red)[32], int& turn) {
+// Pairs of columns in packed f32x2 arithmetic.
+__device__ __forceinline__ float2 bn_f2(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 bn_mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 bn_add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 bn_fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// Eight columns of one thread.
+struct Bn8 {
+    float2 v[4];
+};
+__device__ __forceinline__ Bn8 bn_fill(float v) { return {{bn_f2(v), bn_f2(v), bn_f2(v), bn_f2(v)}}; }
+__device__ __forceinline__ float2 bn_sum4(const Bn8& a) { return bn_add(bn_add(a.v[0], a.v[1]), bn_add(a.v[2], a.v[3])); }
+__device__ __forceinline__ Bn8 bn_unpack(uint4 q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Bn8 r;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    for (int e = 0; e < 4; ++e) r.v[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+    return r;
+}
+__device__ __forceinline__ uint4 bn_pack(const Bn8& a) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a.v[e].x, a.v[e].y);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Stores; the value returned is what the type holds.
+__device__ __forceinline__ Bn8 bn_store8(__nv_bfloat16* p, const Bn8& a, bool store) {
+    const uint4 q = bn_pack(a);
+    if (store) *reinterpret_cast<uint4*>(p) = q;
+    return bn_unpack(q);
+}
+__device__ __forceinline__ Bn8 bn_store8(float* p, const Bn8& a, bool store) {
+    if (store) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+        reinterpret_cast<float4*>(p)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+    }
+    return a;
+}
+__device__ __forceinline__ Bn8 bn_load8(const float* p, float other) {
+    if (!p) return bn_fill(other);
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+}
+
+template <int N>
+__device__ __forceinline__ float bn_shfl_sum(float v) {
+#pragma unroll
+    for (int off = N / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+// The block's sums of a pair, one barrier (`red`: two buffers in turn); at most 16 warps.
+__device__ __forceinline__ float2 bn_block_sum2(float2 v, float2 (*red)[32], int& turn) {
+    v = make_float2(bn_shfl_sum<32>(v.x), bn_shfl_sum<32>(v.y));
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     if (nw == 1) return v;
     float2* r = red[turn];
@@ -359,26 +408,7 @@ __device__ __forceinline__ float2 bn_block_sum2(float2 v, float2 (*red)[32], int
     if (lane == 0) r[threadIdx.x >> 5] = v;
     __syncthreads();
     v = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) {  // at most 16 warps, in both halves
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
-    }
-    return v;
-}
-__device__ __forceinline__ float bn_block_sum(float v, float2 (*red)[32], int& turn) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (nw == 1) return v;
-    float2* r = red[turn];
-    turn ^= 1;
-    if (lane == 0) r[threadIdx.x >> 5].x = v;
-    __syncthreads();
-    v = (lane & 15) < nw ? r[lane & 15].x : 0.f;
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+    return make_float2(bn_shfl_sum<16>(v.x), bn_shfl_sum<16>(v.y));
 }
 
 // 16-byte pieces of eight elements.
@@ -388,160 +418,201 @@ constexpr int kBnPieces = (int)sizeof(T) / 2;
 // A thread's eight columns of a row into its pieces of a stage, and back.
 // Piece q of thread t is at stage + (q * blockDim.x + t) * 16.
 template <typename T>
-__device__ __forceinline__ void bn_fetch(unsigned char* stage, int q, const T* row) {
+__device__ __forceinline__ void bn_fetch(unsigned char* mine, int q, const T* row) {
 #pragma unroll
     for (int h = 0; h < kBnPieces<T>; ++h)
-        cp_async<16>(stage + ((q + h) * blockDim.x + threadIdx.x) * 16, reinterpret_cast<const char*>(row) + 16 * h, true);
+        cp_async<16>(mine + (q + h) * blockDim.x * 16, reinterpret_cast<const char*>(row) + 16 * h, true);
 }
 template <typename T>
-__device__ __forceinline__ void bn_fetched(const unsigned char* stage, int q, float (&v)[8]) {
+__device__ __forceinline__ Bn8 bn_fetched(const unsigned char* mine, int q) {
     if constexpr (sizeof(T) == 2) {
-        bn_load<8>(reinterpret_cast<const __nv_bfloat16*>(stage + (q * blockDim.x + threadIdx.x) * 16), v);
+        return bn_unpack(*reinterpret_cast<const uint4*>(mine + q * blockDim.x * 16));
     } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 a = *reinterpret_cast<const float4*>(stage + ((q + h) * blockDim.x + threadIdx.x) * 16);
-            v[4 * h] = a.x, v[4 * h + 1] = a.y, v[4 * h + 2] = a.z, v[4 * h + 3] = a.w;
-        }
+        const float4 a = *reinterpret_cast<const float4*>(mine + q * blockDim.x * 16);
+        const float4 b = *reinterpret_cast<const float4*>(mine + (q + 1) * blockDim.x * 16);
+        return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
     }
 }
 
 // Vectors of a thread's columns: held in registers for one group of columns,
 // read again a row (they stay in L1) for two.
-template <int K, bool HOLD>
+template <int K>
 struct BnVec {
     const float* p;
     float other;
-    float v[HOLD ? K : 1][8];
-    __device__ __forceinline__ void start(const float* q, float without, int col0, int step, int d) {
+    Bn8 v;
+    __device__ __forceinline__ void start(const float* q, float without, int col0, int d) {
         p = q;
         other = without;
-        if constexpr (HOLD) {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (col0 + k * step < d) bn_vec<8>(p, col0 + k * step, other, v[k]);
-        }
+        if constexpr (K == 1) v = bn_load8(col0 < d ? p ? p + col0 : p : nullptr, other);
     }
-    __device__ __forceinline__ void get(int k, int c, float (&o)[8]) const {
-        if constexpr (HOLD) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = v[k][e];
-        } else {
-            bn_vec<8>(p, c, other, o);
-        }
+    __device__ __forceinline__ Bn8 get(int c) const {
+        if constexpr (K == 1) return v;
+        return bn_load8(p ? p + c : p, other);
     }
 };
 
 template <int K>
 constexpr int kBnStages = K == 1 ? 4 : 2;
+constexpr int kBnFwdRegs = 80;  // 24 warps on an SM
 template <typename TS, typename TU, int K>
 constexpr int kBnFwdPieces = K * (kBnPieces<TS> + kBnPieces<TU>);
 template <typename TS, typename TU, int K>
 constexpr int kBnBwdPieces = K * 2 * (kBnPieces<TS> + kBnPieces<TU>);
 
-template <typename TS, typename TU, int K>
-__global__ void __launch_bounds__(kBlockNormThreads, K == 1 ? 2 : 1) block_norm_fwd_run_kernel(const BlockNormParams p) {
+// Mean (0 with rms) and 1/sigma of the row held in v, one barrier: each warp
+// has the mean and the centred squares of its own columns, and with means m_w
+// of n_w columns the row's squares are sum_w M2_w + n_w (m_w - mean)^2: no
+// difference of large sums.
+template <int K>
+struct BnStats {
+    float own_inv;     // 1 / columns of this warp
+    float n, n_inv;    // columns of warp lane % 16, and 1 over it (0 where there is none)
+    float per, eps;
+    int d, step, rms;
+    __device__ __forceinline__ float columns(int w) const {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) n += max(0, min(256, d - (w * 256 + k * step)));
+        return (float)n;
+    }
+    __device__ __forceinline__ void start(const BlockNormParams& p) {
+        d = p.d, step = blockDim.x * 8, rms = p.rms, eps = p.eps, per = 1.f / (float)p.d;
+        const int w = threadIdx.x & 15, nw = blockDim.x >> 5;
+        own_inv = 1.f / fmaxf(columns(threadIdx.x >> 5), 1.f);
+        n = w < nw ? columns(w) : 0.f;
+        n_inv = n > 0.f ? 1.f / n : 0.f;
+    }
+    __device__ __forceinline__ float2 of(const Bn8 (&v)[K], float2 (*red)[32], int& turn) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        float mine = 0.f, own = 0.f;  // the warp's sum and its mean
+        if (!rms) {
+            float2 s = bn_sum4(v[0]);
+#pragma unroll
+            for (int k = 1; k < K; ++k) s = bn_add(s, bn_sum4(v[k]));  // columns past d hold 0
+            mine = bn_shfl_sum<32>(s.x + s.y);
+            own = mine * own_inv;
+        }
+        float2 q = bn_f2(0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (threadIdx.x * 8 + k * step >= d) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 c = bn_add(v[k].v[e], bn_f2(-own));
+                q = bn_fma(c, c, q);
+            }
+        }
+        float2 w = make_float2(mine, bn_shfl_sum<32>(q.x + q.y));
+        if (nw == 1) return make_float2(own, rsqrtf(w.y * per + eps));
+        float2* r = red[turn];
+        turn ^= 1;
+        if (lane == 0) r[warp] = w;
+        __syncthreads();
+        w = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
+        float mu = 0.f;
+        if (!rms) {
+            mu = bn_shfl_sum<16>(w.x) * per;
+            const float off = w.x * n_inv - mu;
+            w.y = fmaf(n * off, off, w.y);
+        }
+        return make_float2(mu, rsqrtf(bn_shfl_sum<16>(w.y) * per + eps));
+    }
+};
+
+template <typename TS, typename TU, int K, bool POST>
+__global__ void __maxnreg__(kBnFwdRegs) block_norm_fwd_run_kernel(const BlockNormParams p) {
     constexpr int NS = kBnStages<K>, PIECES = kBnFwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
     extern __shared__ __align__(16) unsigned char bn_smem[];
     __shared__ float2 red[2][32];
     int turn = 0;
     const int64_t b = blockIdx.y;
     const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
-    const int64_t r0 = b * p.L + p.L * seg / p.nseg, r1 = b * p.L + p.L * (seg + 1) / p.nseg;
-    auto fetch = [&](int64_t row, int s) {
-        if (row < r1) {
-            unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+    const int64_t r0 = b * p.L + p.L * seg / p.nseg;
+    const int rows = (int)(b * p.L + p.L * (seg + 1) / p.nseg - r0);
+    unsigned char* const mine = bn_smem + threadIdx.x * 16;
+    const int stage_bytes = PIECES * blockDim.x * 16;
+    const TS* x_in = static_cast<const TS*>(p.x) + r0 * d + col0;   // the next row to copy
+    const TU* u_in = p.u ? static_cast<const TU*>(p.u) + r0 * d + col0 : nullptr;
+    auto fetch = [&](int row, int s) {
+        if (row < rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = col0 + k * step;
-                if (c >= d) continue;
-                bn_fetch(stage, k * (PS + PU), static_cast<const TS*>(p.x) + row * d + c);
-                if (p.u) bn_fetch(stage, k * (PS + PU) + PS, static_cast<const TU*>(p.u) + row * d + c);
+                if (col0 + k * step >= d) continue;
+                bn_fetch(mine + s * stage_bytes, k * (PS + PU), x_in + k * step);
+                if (u_in) bn_fetch(mine + s * stage_bytes, k * (PS + PU) + PS, u_in + k * step);
             }
+            x_in += d;
+            if (u_in) u_in += d;
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < NS; ++s) fetch(r0 + s, s);
-    BnVec<K, K == 1> gate, post_w, gamma, beta;
-    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
-    post_w.start(p.post_w, 1.f, col0, step, d);
-    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
-    beta.start(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, col0, step, d);
-    const float per = 1.f / (float)d;
-    // mean (0 with rms) and 1/sigma of the row held in v
-    auto stats = [&](const float (&v)[K][8], float& mu, float& rs) {
-        mu = 0.f;
-        if (!p.rms) {
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s += v[k][e];  // columns past d hold 0
-            mu = bn_block_sum(s, red, turn) * per;
-        }
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (col0 + k * step < d) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q = fmaf(v[k][e] - mu, v[k][e] - mu, q);
-            }
-        rs = rsqrtf(bn_block_sum(q, red, turn) * per + p.eps);
-    };
+    for (int s = 0; s < NS; ++s) fetch(s, s);
+    BnVec<K> gate, post_w, gamma, beta;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, d);
+    if (POST) post_w.start(p.post_w, 1.f, col0, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, d);
+    beta.start(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, col0, d);
+    const float2 res = bn_f2(p.res_scale);
+    BnStats<K> row_stats;
+    row_stats.start(p);
+    TS* x_out = p.x_out ? static_cast<TS*>(p.x_out) + r0 * d + col0 : nullptr;
+    TU* y = p.y ? static_cast<TU*>(p.y) + r0 * d + col0 : nullptr;
     int s = 0;
-    for (int64_t row = r0; row < r1; ++row) {
-        const unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+    for (int row = 0; row < rows; ++row) {
+        unsigned char* const stage = mine + s * stage_bytes;
         cp_async_wait_pending<NS - 1>();
-        float x[K][8], u[K][8];
-        float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
+        Bn8 x[K], u[K];
+        float2 sx = make_float2(0.f, 1.f), su = make_float2(0.f, 1.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] = u[k][e] = 0.f;
+            x[k] = u[k] = bn_fill(0.f);
             if (col0 + k * step < d) {
-                bn_fetched<TS>(stage, k * (PS + PU), x[k]);
-                if (p.u) bn_fetched<TU>(stage, k * (PS + PU) + PS, u[k]);
+                x[k] = bn_fetched<TS>(stage, k * (PS + PU));
+                if (u_in) u[k] = bn_fetched<TU>(stage, k * (PS + PU) + PS);
             }
         }
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
-        if (p.post_w) stats(u, st.z, st.w);
+        if constexpr (POST) su = row_stats.of(u, red, turn);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = col0 + k * step;
             if (c >= d) continue;
-            float g[8];
-            if (p.post_w) {
-                post_w.get(k, c, g);
+            const Bn8 g = gate.get(c);
+            if constexpr (POST) {
+                const Bn8 w = post_w.get(c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[k][e] = (u[k][e] - st.z) * st.w * g[e];
+                for (int e = 0; e < 4; ++e)
+                    u[k].v[e] = bn_mul(bn_mul(bn_add(u[k].v[e], bn_f2(-su.x)), bn_f2(su.y)), w.v[e]);
             }
-            gate.get(k, c, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] = bn_round<TS>(fmaf(g[e], u[k][e], p.res_scale * x[k][e]));
-            if (p.x_out) bn_store<8>(static_cast<TS*>(p.x_out) + row * d + c, x[k]);
+            for (int e = 0; e < 4; ++e) x[k].v[e] = bn_fma(g.v[e], u[k].v[e], bn_mul(res, x[k].v[e]));
+            x[k] = bn_store8(x_out + k * step, x[k], x_out != nullptr);
         }
-        if (p.y) {
-            stats(x, st.x, st.y);
+        if (y) {
+            sx = row_stats.of(x, red, turn);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = col0 + k * step;
                 if (c >= d) continue;
-                float g[8], be[8];
-                gamma.get(k, c, g);
-                beta.get(k, c, be);
+                const Bn8 g = gamma.get(c), be = beta.get(c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = fmaf(g[e], (x[k][e] - st.x) * st.y, be[e]);
-                bn_store<8>(static_cast<TU*>(p.y) + row * d + c, x[k]);
+                for (int e = 0; e < 4; ++e)
+                    x[k].v[e] = bn_fma(g.v[e], bn_mul(bn_add(x[k].v[e], bn_f2(-sx.x)), bn_f2(sx.y)), be.v[e]);
+                bn_store8(y + k * step, x[k], true);
             }
+            y += d;
         }
-        if (p.stats && threadIdx.x == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
+        if (x_out) x_out += d;
+        if (p.stats && threadIdx.x == 0)
+            reinterpret_cast<float4*>(p.stats)[r0 + row] = make_float4(sx.x, sx.y, su.x, su.y);
     }
     cp_async_wait_all();
 }
 
-template <typename TS, typename TU, int K>
+template <typename TS, typename TU, int K, bool POST>
 __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(const BlockNormParams p) {
     constexpr int NS = kBnStages<K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
     extern __shared__ __align__(16) unsigned char bn_smem[];
@@ -549,122 +620,134 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     int turn = 0;
     const int64_t b = blockIdx.y;
     const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
-    const int64_t r0 = b * p.L + p.L * seg / p.nseg, r1 = b * p.L + p.L * (seg + 1) / p.nseg;
-    auto fetch = [&](int64_t row, int s) {
-        if (row < r1) {
-            unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
+    const int64_t r0 = b * p.L + p.L * seg / p.nseg;
+    const int rows = (int)(b * p.L + p.L * (seg + 1) / p.nseg - r0);
+    unsigned char* const mine = bn_smem + threadIdx.x * 16;
+    const int stage_bytes = PIECES * blockDim.x * 16;
+    int64_t at = r0 * d + col0;  // the next row to copy
+    auto fetch = [&](int row, int s) {
+        if (row < rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = col0 + k * step, q = k * 2 * (PS + PU);
-                if (c >= d) continue;
+                const int q = k * 2 * (PS + PU);
+                if (col0 + k * step >= d) continue;
+                const int64_t c = at + k * step;
+                unsigned char* const stage = mine + s * stage_bytes;
                 if (p.dy) {
-                    bn_fetch(stage, q, static_cast<const TS*>(p.x) + row * d + c);
-                    bn_fetch(stage, q + PS, static_cast<const TU*>(p.dy) + row * d + c);
+                    bn_fetch(stage, q, static_cast<const TS*>(p.x) + c);
+                    bn_fetch(stage, q + PS, static_cast<const TU*>(p.dy) + c);
                 }
-                if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + row * d + c);
-                if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + row * d + c);
+                if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + c);
+                if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + c);
             }
+            at += d;
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < NS; ++s) fetch(r0 + s, s);
-    BnVec<K, K == 1> gate, post_w, gamma;
-    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
-    post_w.start(p.post_w, 1.f, col0, step, d);
-    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
+    for (int s = 0; s < NS; ++s) fetch(s, s);
+    BnVec<K> gate, post_w, gamma;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, d);
+    if (POST) post_w.start(p.post_w, 1.f, col0, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, d);
     const float per = 1.f / (float)d;
-    float sg[K][8], sw[K][8], sm[K][8], sb[K][8];
+    const float2 res = bn_f2(p.res_scale);
+    Bn8 sg[K], sw[K], sm[K], sb[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sg[k][e] = sw[k][e] = sm[k][e] = sb[k][e] = 0.f;
+    for (int k = 0; k < K; ++k) sg[k] = sw[k] = sm[k] = sb[k] = bn_fill(0.f);
+    TS* dx = static_cast<TS*>(p.dx) + r0 * d + col0;
+    TU* du = p.u ? static_cast<TU*>(p.du) + r0 * d + col0 : nullptr;
+    const float4* stats = reinterpret_cast<const float4*>(p.stats) + r0;
+    float4 ahead = rows > 0 ? stats[0] : make_float4(0.f, 0.f, 0.f, 0.f);
     int s = 0;
-    for (int64_t row = r0; row < r1; ++row) {
-        const unsigned char* stage = bn_smem + s * PIECES * blockDim.x * 16;
-        const float4 st = reinterpret_cast<const float4*>(p.stats)[row];
+    for (int row = 0; row < rows; ++row) {
+        unsigned char* const stage = mine + s * stage_bytes;
+        const float4 st = ahead;
+        if (row + 1 < rows) ahead = stats[row + 1];
         cp_async_wait_pending<NS - 1>();
-        float n[K][8], dy[K][8], D[K][8];
-        float2 sum = make_float2(0.f, 0.f);
+        Bn8 n[K], dy[K], D[K];
+        float2 sum = bn_f2(0.f);
         if (p.dy) {
+            float2 s1 = bn_f2(0.f), s2 = bn_f2(0.f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = col0 + k * step, q = k * 2 * (PS + PU);
                 if (c >= d) continue;
-                bn_fetched<TS>(stage, q, n[k]);
-                bn_fetched<TU>(stage, q + PS, dy[k]);
-                float ga[8];
-                gamma.get(k, c, ga);
+                n[k] = bn_fetched<TS>(stage, q);
+                dy[k] = bn_fetched<TU>(stage, q + PS);
+                const Bn8 ga = gamma.get(c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[k][e] = (n[k][e] - st.x) * st.y;
-                    sm[k][e] = fmaf(dy[k][e], n[k][e], sm[k][e]);
-                    sb[k][e] += dy[k][e];
-                    dy[k][e] *= ga[e];
-                    sum.x += dy[k][e];
-                    sum.y = fmaf(dy[k][e], n[k][e], sum.y);
+                for (int e = 0; e < 4; ++e) {
+                    n[k].v[e] = bn_mul(bn_add(n[k].v[e], bn_f2(-st.x)), bn_f2(st.y));
+                    sm[k].v[e] = bn_fma(dy[k].v[e], n[k].v[e], sm[k].v[e]);
+                    sb[k].v[e] = bn_add(sb[k].v[e], dy[k].v[e]);
+                    dy[k].v[e] = bn_mul(dy[k].v[e], ga.v[e]);
+                    s1 = bn_add(s1, dy[k].v[e]);
+                    s2 = bn_fma(dy[k].v[e], n[k].v[e], s2);
                 }
             }
-            sum = bn_block_sum2(sum, red, turn);
+            sum = bn_block_sum2(make_float2(s1.x + s1.y, s2.x + s2.y), red, turn);
             sum = make_float2(p.rms ? 0.f : sum.x * per, sum.y * per);
         }
-        float2 tu = make_float2(0.f, 0.f);
-        float u[K][8];
+        float2 t1 = bn_f2(0.f), t2 = bn_f2(0.f);
+        Bn8 u[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = col0 + k * step, q = k * 2 * (PS + PU);
             if (c >= d) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) D[k][e] = 0.f;
-            if (p.dx_out) bn_fetched<TS>(stage, q + PS + PU, D[k]);
-            if (p.u) bn_fetched<TU>(stage, q + 2 * PS + PU, u[k]);
+            D[k] = p.dx_out ? bn_fetched<TS>(stage, q + PS + PU) : bn_fill(0.f);
             if (p.dy) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) D[k][e] = fmaf(st.y, dy[k][e] - fmaf(n[k][e], sum.y, sum.x), D[k][e]);
+                for (int e = 0; e < 4; ++e)
+                    D[k].v[e] = bn_fma(bn_f2(st.y),
+                                       bn_add(dy[k].v[e], bn_fma(n[k].v[e], bn_f2(-sum.y), bn_f2(-sum.x))), D[k].v[e]);
             }
-            float o[8];
+            Bn8 o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = p.res_scale * D[k][e];
-            bn_store<8>(static_cast<TS*>(p.dx) + row * d + c, o);
-            if (!p.u) continue;
-            float ga[8], w[8];
-            gate.get(k, c, ga);
-            if (p.post_w) {
-                post_w.get(k, c, w);
+            for (int e = 0; e < 4; ++e) o.v[e] = bn_mul(res, D[k].v[e]);
+            bn_store8(dx + k * step, o, true);
+            if (!du) continue;
+            u[k] = bn_fetched<TU>(stage, q + 2 * PS + PU);
+            const Bn8 ga = gate.get(c);
+            if constexpr (POST) {
+                const Bn8 w = post_w.get(c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float m = (u[k][e] - st.z) * st.w, g = ga[e] * D[k][e], gw = g * w[e];
-                    sg[k][e] = fmaf(D[k][e], m * w[e], sg[k][e]);
-                    sw[k][e] = fmaf(g, m, sw[k][e]);
-                    tu.x += gw;
-                    tu.y = fmaf(gw, m, tu.y);
-                    u[k][e] = m;
-                    D[k][e] = gw;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 m = bn_mul(bn_add(u[k].v[e], bn_f2(-st.z)), bn_f2(st.w));
+                    const float2 g = bn_mul(ga.v[e], D[k].v[e]), gw = bn_mul(g, w.v[e]);
+                    sg[k].v[e] = bn_fma(D[k].v[e], bn_mul(m, w.v[e]), sg[k].v[e]);
+                    sw[k].v[e] = bn_fma(g, m, sw[k].v[e]);
+                    t1 = bn_add(t1, gw);
+                    t2 = bn_fma(gw, m, t2);
+                    u[k].v[e] = m;
+                    D[k].v[e] = gw;
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sg[k][e] = fmaf(D[k][e], u[k][e], sg[k][e]);
-                    o[e] = ga[e] * D[k][e];
+                for (int e = 0; e < 4; ++e) {
+                    sg[k].v[e] = bn_fma(D[k].v[e], u[k].v[e], sg[k].v[e]);
+                    o.v[e] = bn_mul(ga.v[e], D[k].v[e]);
                 }
-                bn_store<8>(static_cast<TU*>(p.du) + row * d + c, o);
+                bn_store8(du + k * step, o, true);
             }
         }
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
-        if (p.u && p.post_w) {
-            tu = bn_block_sum2(tu, red, turn);
+        if constexpr (POST) {
+            float2 tu = bn_block_sum2(make_float2(t1.x + t1.y, t2.x + t2.y), red, turn);
             tu = make_float2(p.rms ? 0.f : tu.x * per, tu.y * per);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = col0 + k * step;
-                if (c >= d) continue;
-                float o[8];
+                if (col0 + k * step >= d) continue;
+                Bn8 o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = st.w * (D[k][e] - fmaf(u[k][e], tu.y, tu.x));
-                bn_store<8>(static_cast<TU*>(p.du) + row * d + c, o);
+                for (int e = 0; e < 4; ++e)
+                    o.v[e] = bn_mul(bn_f2(st.w), bn_add(D[k].v[e], bn_fma(u[k].v[e], bn_f2(-tu.y), bn_f2(-tu.x))));
+                bn_store8(du + k * step, o, true);
             }
         }
+        dx += d;
+        if (du) du += d;
     }
     cp_async_wait_all();
     if (!p.part) return;
@@ -673,10 +756,10 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     for (int k = 0; k < K; ++k) {
         const int c = col0 + k * step;
         if (c >= d) continue;
-        bn_store<8>(q + c, sg[k]);
-        bn_store<8>(q + d + c, sw[k]);
-        bn_store<8>(q + 2 * (int64_t)d + c, sm[k]);
-        bn_store<8>(q + 3 * (int64_t)d + c, sb[k]);
+        bn_store8(q + c, sg[k], true);
+        bn_store8(q + d + c, sw[k], true);
+        bn_store8(q + 2 * (int64_t)d + c, sm[k], true);
+        bn_store8(q + 3 * (int64_t)d + c, sb[k], true);
     }
 }
 

@@ -108,13 +108,16 @@ bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     if (smem > kMaxRunSmem) return false;
     void (*fn)(BlockNormParams);
     if constexpr (BWD)
-        fn = bimamba::block_norm_bwd_run_kernel<TS, TU, K>;
+        fn = k.post_w ? bimamba::block_norm_bwd_run_kernel<TS, TU, K, true>
+                      : bimamba::block_norm_bwd_run_kernel<TS, TU, K, false>;
     else
-        fn = bimamba::block_norm_fwd_run_kernel<TS, TU, K>;
+        fn = k.post_w ? bimamba::block_norm_fwd_run_kernel<TS, TU, K, true>
+                      : bimamba::block_norm_fwd_run_kernel<TS, TU, K, false>;
     // one limit for all widths: it is raised once a kernel
     if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), kMaxRunSmem))) return true;
-    if (!BWD) {  // one run a block that an SM holds (64 registers a thread, 128 for K = 2)
-        const int held = (int)std::min<size_t>(std::min(1024 / K / threads, 16), 220 * 1024 / (smem + 2048));
+    if (!BWD) {  // one run a block that an SM holds
+        const int by_regs = 65536 / (bimamba::kBnFwdRegs * threads);
+        const int held = (int)std::min<size_t>(std::min(by_regs, 24), 220 * 1024 / (smem + 2048));
         k.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(k.L, (int64_t)kSms * std::max(held, 1) / k.batch));
     }
     fn<<<dim3((unsigned)k.nseg, (unsigned)k.batch), threads, smem, st>>>(k);
