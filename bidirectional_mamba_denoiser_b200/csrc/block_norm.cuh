@@ -392,23 +392,46 @@ __device__ __forceinline__ Bn8 bn_load8(const float* p, float other) {
     return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
-template <int N>
-__device__ __forceinline__ float bn_shfl_sum(float v) {
+__device__ __forceinline__ float bn_warp_sum(float v) {
 #pragma unroll
-    for (int off = N / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
-// The block's sums of a pair, one barrier (`red`: two buffers in turn); at most 16 warps.
-__device__ __forceinline__ float2 bn_block_sum2(float2 v, float2 (*red)[32], int& turn) {
-    v = make_float2(bn_shfl_sum<32>(v.x), bn_shfl_sum<32>(v.y));
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (nw == 1) return v;
-    float2* r = red[turn];
-    turn ^= 1;
-    if (lane == 0) r[threadIdx.x >> 5] = v;
+// What a block's warps hand one another for row sums: two buffers in turn, so
+// that one barrier a sum is enough.  At most 16 warps, the absent ones zeros;
+// every thread adds the warps' values itself, in order (a read of two warps'
+// pairs is one broadcast; shuffles would cost more).
+struct BnShared {
+    float4 part[2][8];  // (sum, squares) of each warp
+    float4 count[8];    // (columns, 1 / columns) of each warp
+};
+// `columns` of this warp; before the block's first sum.
+__device__ __forceinline__ void bn_share(BnShared& sh, float columns) {
+    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float2* part = reinterpret_cast<float2*>(sh.part);
+    float2* count = reinterpret_cast<float2*>(sh.count);
+    if (threadIdx.x < 32) part[threadIdx.x] = make_float2(0.f, 0.f);
+    if (threadIdx.x >= nw && threadIdx.x < 16) count[threadIdx.x] = make_float2(0.f, 0.f);
+    if ((threadIdx.x & 31) == 0) count[warp] = make_float2(columns, columns > 0.f ? 1.f / columns : 0.f);
     __syncthreads();
-    v = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
-    return make_float2(bn_shfl_sum<16>(v.x), bn_shfl_sum<16>(v.y));
+}
+// The block's sums of a pair.
+__device__ __forceinline__ float2 bn_block_sum2(float2 v, BnShared& sh, int& turn) {
+    v = make_float2(bn_warp_sum(v.x), bn_warp_sum(v.y));
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    float4* r = sh.part[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(r)[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (2 * w >= nw) break;
+        const float4 a = r[w];
+        v = bn_add(bn_add(v, make_float2(a.x, a.y)), make_float2(a.z, a.w));
+    }
+    return v;
 }
 
 // 16-byte pieces of eight elements.
@@ -434,29 +457,46 @@ __device__ __forceinline__ Bn8 bn_fetched(const unsigned char* mine, int q) {
     }
 }
 
-// Vectors of a thread's columns: held in registers for one group of columns,
-// read again a row (they stay in L1) for two.
-template <int K>
+// Zeros in the pieces of a thread that no copy fills: all of a group past the
+// last column, and from piece `from` on without `more`.
+template <int K, int NS, int PER>
+__device__ __forceinline__ void bn_clear(unsigned char* mine, const bool (&in)[K], bool more, int from) {
+    for (int q = 0; q < NS * K * PER; ++q)
+        if (!in[q / PER % K] || (!more && q % PER >= from))
+            *reinterpret_cast<uint4*>(mine + q * blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Vectors of a thread's columns: held in registers, or (where there are too
+// many columns) read again a row; they stay in L1.
+template <int K, bool HOLD>
 struct BnVec {
     const float* p;
     float other;
-    Bn8 v;
-    __device__ __forceinline__ void start(const float* q, float without, int col0, int d) {
+    Bn8 v[HOLD ? K : 1];
+    __device__ __forceinline__ void start(const float* q, float without, int col0, int step, int d) {
         p = q;
         other = without;
-        if constexpr (K == 1) v = bn_load8(col0 < d ? p ? p + col0 : p : nullptr, other);
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = col0 + k * step;
+                v[k] = bn_load8(p && c < d ? p + c : nullptr, c < d ? other : 0.f);  // zeros keep zeros past d
+            }
+        }
     }
-    __device__ __forceinline__ Bn8 get(int c) const {
-        if constexpr (K == 1) return v;
+    __device__ __forceinline__ Bn8 get(int k, int c) const {
+        if constexpr (HOLD) return v[k];
         return bn_load8(p ? p + c : p, other);
     }
 };
 
-template <int K>
-constexpr int kBnStages = K == 1 ? 4 : 2;
-constexpr int kBnFwdRegs = 80;  // 24 warps on an SM
+// Rows ahead, and the 16-byte pieces of one: what fits in shared memory.
+template <typename TS, typename TU>
+constexpr int kBnFwdStages = sizeof(TU) == 4 ? 3 : 4;
 template <typename TS, typename TU, int K>
 constexpr int kBnFwdPieces = K * (kBnPieces<TS> + kBnPieces<TU>);
+template <int K>
+constexpr int kBnBwdStages = K == 1 ? 4 : 2;
 template <typename TS, typename TU, int K>
 constexpr int kBnBwdPieces = K * 2 * (kBnPieces<TS> + kBnPieces<TU>);
 
@@ -465,98 +505,105 @@ constexpr int kBnBwdPieces = K * 2 * (kBnPieces<TS> + kBnPieces<TU>);
 // of n_w columns the row's squares are sum_w M2_w + n_w (m_w - mean)^2: no
 // difference of large sums.
 template <int K>
-struct BnStats {
-    float own_inv;     // 1 / columns of this warp
-    float n, n_inv;    // columns of warp lane % 16, and 1 over it (0 where there is none)
-    float per, eps;
-    int d, step, rms;
-    __device__ __forceinline__ float columns(int w) const {
-        int n = 0;
+__device__ __forceinline__ float bn_warp_columns(int d) {
+    int n = 0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) n += max(0, min(256, d - (w * 256 + k * step)));
-        return (float)n;
+    for (int k = 0; k < K; ++k)
+        n += max(0, min(256, d - (int)((threadIdx.x >> 5) * 256 + k * blockDim.x * 8)));
+    return (float)n;
+}
+template <int K>
+__device__ __forceinline__ float2 bn_row_stats(const Bn8 (&v)[K], const bool (&in)[K], const BlockNormParams& p, float own_inv, BnShared& sh,
+                                               int& turn) {
+    const int nw = blockDim.x >> 5;
+    const float per = 1.f / (float)p.d;
+    float sum = 0.f, own = 0.f;  // the warp's sum and its mean
+    if (!p.rms) {
+        float2 s = bn_sum4(v[0]);
+#pragma unroll
+        for (int k = 1; k < K; ++k) s = bn_add(s, bn_sum4(v[k]));  // columns past d hold 0
+        sum = bn_warp_sum(s.x + s.y);
+        own = sum * own_inv;
     }
-    __device__ __forceinline__ void start(const BlockNormParams& p) {
-        d = p.d, step = blockDim.x * 8, rms = p.rms, eps = p.eps, per = 1.f / (float)p.d;
-        const int w = threadIdx.x & 15, nw = blockDim.x >> 5;
-        own_inv = 1.f / fmaxf(columns(threadIdx.x >> 5), 1.f);
-        n = w < nw ? columns(w) : 0.f;
-        n_inv = n > 0.f ? 1.f / n : 0.f;
+    float2 q = bn_f2(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (!in[k]) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 c = bn_add(v[k].v[e], bn_f2(-own));
+            q = bn_fma(c, c, q);
+        }
     }
-    __device__ __forceinline__ float2 of(const Bn8 (&v)[K], float2 (*red)[32], int& turn) const {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-        float mine = 0.f, own = 0.f;  // the warp's sum and its mean
-        if (!rms) {
-            float2 s = bn_sum4(v[0]);
+    const float squares = bn_warp_sum(q.x + q.y);
+    if (nw == 1) return make_float2(own, rsqrtf(squares * per + p.eps));
+    float4* r = sh.part[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(r)[threadIdx.x >> 5] = make_float2(sum, squares);
+    __syncthreads();
+    float2 total = bn_f2(0.f);
 #pragma unroll
-            for (int k = 1; k < K; ++k) s = bn_add(s, bn_sum4(v[k]));  // columns past d hold 0
-            mine = bn_shfl_sum<32>(s.x + s.y);
-            own = mine * own_inv;
-        }
-        float2 q = bn_f2(0.f);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (threadIdx.x * 8 + k * step >= d) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 c = bn_add(v[k].v[e], bn_f2(-own));
-                q = bn_fma(c, c, q);
-            }
-        }
-        float2 w = make_float2(mine, bn_shfl_sum<32>(q.x + q.y));
-        if (nw == 1) return make_float2(own, rsqrtf(w.y * per + eps));
-        float2* r = red[turn];
-        turn ^= 1;
-        if (lane == 0) r[warp] = w;
-        __syncthreads();
-        w = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
-        float mu = 0.f;
-        if (!rms) {
-            mu = bn_shfl_sum<16>(w.x) * per;
-            const float off = w.x * n_inv - mu;
-            w.y = fmaf(n * off, off, w.y);
-        }
-        return make_float2(mu, rsqrtf(bn_shfl_sum<16>(w.y) * per + eps));
+    for (int w = 0; w < 8; ++w) {
+        if (2 * w >= nw) break;
+        const float4 a = r[w];
+        total = bn_add(bn_add(total, make_float2(a.x, a.y)), make_float2(a.z, a.w));
     }
-};
+    const float mu = total.x * per;
+    if (!p.rms) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (2 * w >= nw) break;
+            const float4 a = r[w], n = sh.count[w];
+            const float o0 = fmaf(a.x, n.y, -mu), o1 = fmaf(a.z, n.w, -mu);
+            total.y = fmaf(n.x * o0, o0, fmaf(n.z * o1, o1, total.y));
+        }
+    }
+    return make_float2(p.rms ? 0.f : mu, rsqrtf(total.y * per + p.eps));
+}
 
 template <typename TS, typename TU, int K, bool POST>
-__global__ void __maxnreg__(kBnFwdRegs) block_norm_fwd_run_kernel(const BlockNormParams p) {
-    constexpr int NS = kBnStages<K>, PIECES = kBnFwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
+__global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_run_kernel(const BlockNormParams p) {
+    constexpr int NS = kBnFwdStages<TS, TU>, PIECES = kBnFwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
     extern __shared__ __align__(16) unsigned char bn_smem[];
-    __shared__ float2 red[2][32];
+    __shared__ BnShared sh;
     int turn = 0;
     const int64_t b = blockIdx.y;
     const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
-    const int64_t r0 = b * p.L + p.L * seg / p.nseg;
-    const int rows = (int)(b * p.L + p.L * (seg + 1) / p.nseg - r0);
+    // rows seg, seg + nseg, ...: the blocks move through memory together
+    const int64_t r0 = b * p.L + seg, hop = (int64_t)p.nseg * d;
+    const int rows = (int)((p.L - seg + p.nseg - 1) / p.nseg);
     unsigned char* const mine = bn_smem + threadIdx.x * 16;
     const int stage_bytes = PIECES * blockDim.x * 16;
     const TS* x_in = static_cast<const TS*>(p.x) + r0 * d + col0;   // the next row to copy
     const TU* u_in = p.u ? static_cast<const TU*>(p.u) + r0 * d + col0 : nullptr;
+    bool in[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) in[k] = col0 + k * step < d;
+    // what is never copied (columns past d, an absent branch) reads as zeros
+    bn_clear<K, NS, PS + PU>(mine, in, u_in != nullptr, PS);
     auto fetch = [&](int row, int s) {
         if (row < rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (col0 + k * step >= d) continue;
+                if (!in[k]) continue;
                 bn_fetch(mine + s * stage_bytes, k * (PS + PU), x_in + k * step);
                 if (u_in) bn_fetch(mine + s * stage_bytes, k * (PS + PU) + PS, u_in + k * step);
             }
-            x_in += d;
-            if (u_in) u_in += d;
+            x_in += hop;
+            if (u_in) u_in += hop;
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < NS; ++s) fetch(s, s);
-    BnVec<K> gate, post_w, gamma, beta;
-    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, d);
-    if (POST) post_w.start(p.post_w, 1.f, col0, d);
-    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, d);
-    beta.start(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, col0, d);
+    BnVec<K, true> gate, post_w, gamma, beta;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
+    if (POST) post_w.start(p.post_w, 1.f, col0, step, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
+    beta.start(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, col0, step, d);
     const float2 res = bn_f2(p.res_scale);
-    BnStats<K> row_stats;
-    row_stats.start(p);
+    const float columns = bn_warp_columns<K>(d), own_inv = 1.f / fmaxf(columns, 1.f);
+    bn_share(sh, columns);
     TS* x_out = p.x_out ? static_cast<TS*>(p.x_out) + r0 * d + col0 : nullptr;
     TU* y = p.y ? static_cast<TU*>(p.y) + r0 * d + col0 : nullptr;
     int s = 0;
@@ -567,61 +614,57 @@ __global__ void __maxnreg__(kBnFwdRegs) block_norm_fwd_run_kernel(const BlockNor
         float2 sx = make_float2(0.f, 1.f), su = make_float2(0.f, 1.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            x[k] = u[k] = bn_fill(0.f);
-            if (col0 + k * step < d) {
-                x[k] = bn_fetched<TS>(stage, k * (PS + PU));
-                if (u_in) u[k] = bn_fetched<TU>(stage, k * (PS + PU) + PS);
-            }
+            x[k] = bn_fetched<TS>(stage, k * (PS + PU));
+            u[k] = bn_fetched<TU>(stage, k * (PS + PU) + PS);
         }
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
-        if constexpr (POST) su = row_stats.of(u, red, turn);
+        if constexpr (POST) su = bn_row_stats<K>(u, in, p, own_inv, sh, turn);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = col0 + k * step;
-            if (c >= d) continue;
-            const Bn8 g = gate.get(c);
+            const Bn8 g = gate.get(k, c);
             if constexpr (POST) {
-                const Bn8 w = post_w.get(c);
+                const Bn8 w = post_w.get(k, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     u[k].v[e] = bn_mul(bn_mul(bn_add(u[k].v[e], bn_f2(-su.x)), bn_f2(su.y)), w.v[e]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[k].v[e] = bn_fma(g.v[e], u[k].v[e], bn_mul(res, x[k].v[e]));
-            x[k] = bn_store8(x_out + k * step, x[k], x_out != nullptr);
+            x[k] = bn_store8(x_out + k * step, x[k], x_out && in[k]);
         }
         if (y) {
-            sx = row_stats.of(x, red, turn);
+            sx = bn_row_stats<K>(x, in, p, own_inv, sh, turn);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = col0 + k * step;
-                if (c >= d) continue;
-                const Bn8 g = gamma.get(c), be = beta.get(c);
+                const Bn8 g = gamma.get(k, c), be = beta.get(k, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[k].v[e] = bn_fma(g.v[e], bn_mul(bn_add(x[k].v[e], bn_f2(-sx.x)), bn_f2(sx.y)), be.v[e]);
-                bn_store8(y + k * step, x[k], true);
+                bn_store8(y + k * step, x[k], in[k]);
             }
-            y += d;
+            y += hop;
         }
-        if (x_out) x_out += d;
+        if (x_out) x_out += hop;
         if (p.stats && threadIdx.x == 0)
-            reinterpret_cast<float4*>(p.stats)[r0 + row] = make_float4(sx.x, sx.y, su.x, su.y);
+            reinterpret_cast<float4*>(p.stats)[r0 + (int64_t)row * p.nseg] = make_float4(sx.x, sx.y, su.x, su.y);
     }
     cp_async_wait_all();
 }
 
 template <typename TS, typename TU, int K, bool POST>
 __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(const BlockNormParams p) {
-    constexpr int NS = kBnStages<K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
+    constexpr int NS = kBnBwdStages<K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
     extern __shared__ __align__(16) unsigned char bn_smem[];
-    __shared__ float2 red[2][32];
+    __shared__ BnShared sh;
     int turn = 0;
     const int64_t b = blockIdx.y;
     const int seg = blockIdx.x, d = p.d, col0 = threadIdx.x * 8, step = blockDim.x * 8;
-    const int64_t r0 = b * p.L + p.L * seg / p.nseg;
-    const int rows = (int)(b * p.L + p.L * (seg + 1) / p.nseg - r0);
+    // rows seg, seg + nseg, ...: the blocks move through memory together
+    const int64_t r0 = b * p.L + seg, hop = (int64_t)p.nseg * d;
+    const int rows = (int)((p.L - seg + p.nseg - 1) / p.nseg);
     unsigned char* const mine = bn_smem + threadIdx.x * 16;
     const int stage_bytes = PIECES * blockDim.x * 16;
     int64_t at = r0 * d + col0;  // the next row to copy
@@ -640,18 +683,19 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
                 if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + c);
                 if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + c);
             }
-            at += d;
+            at += hop;
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < NS; ++s) fetch(s, s);
-    BnVec<K> gate, post_w, gamma;
-    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, d);
-    if (POST) post_w.start(p.post_w, 1.f, col0, d);
-    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, d);
+    BnVec<K, K == 1> gate, post_w, gamma;
+    gate.start(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, col0, step, d);
+    if (POST) post_w.start(p.post_w, 1.f, col0, step, d);
+    gamma.start(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, col0, step, d);
     const float per = 1.f / (float)d;
     const float2 res = bn_f2(p.res_scale);
+    bn_share(sh, 0.f);
     Bn8 sg[K], sw[K], sm[K], sb[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) sg[k] = sw[k] = sm[k] = sb[k] = bn_fill(0.f);
@@ -663,7 +707,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     for (int row = 0; row < rows; ++row) {
         unsigned char* const stage = mine + s * stage_bytes;
         const float4 st = ahead;
-        if (row + 1 < rows) ahead = stats[row + 1];
+        if (row + 1 < rows) ahead = stats[(int64_t)(row + 1) * p.nseg];
         cp_async_wait_pending<NS - 1>();
         Bn8 n[K], dy[K], D[K];
         float2 sum = bn_f2(0.f);
@@ -675,7 +719,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
                 if (c >= d) continue;
                 n[k] = bn_fetched<TS>(stage, q);
                 dy[k] = bn_fetched<TU>(stage, q + PS);
-                const Bn8 ga = gamma.get(c);
+                const Bn8 ga = gamma.get(k, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     n[k].v[e] = bn_mul(bn_add(n[k].v[e], bn_f2(-st.x)), bn_f2(st.y));
@@ -686,7 +730,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
                     s2 = bn_fma(dy[k].v[e], n[k].v[e], s2);
                 }
             }
-            sum = bn_block_sum2(make_float2(s1.x + s1.y, s2.x + s2.y), red, turn);
+            sum = bn_block_sum2(make_float2(s1.x + s1.y, s2.x + s2.y), sh, turn);
             sum = make_float2(p.rms ? 0.f : sum.x * per, sum.y * per);
         }
         float2 t1 = bn_f2(0.f), t2 = bn_f2(0.f);
@@ -708,9 +752,9 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
             bn_store8(dx + k * step, o, true);
             if (!du) continue;
             u[k] = bn_fetched<TU>(stage, q + 2 * PS + PU);
-            const Bn8 ga = gate.get(c);
+            const Bn8 ga = gate.get(k, c);
             if constexpr (POST) {
-                const Bn8 w = post_w.get(c);
+                const Bn8 w = post_w.get(k, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 m = bn_mul(bn_add(u[k].v[e], bn_f2(-st.z)), bn_f2(st.w));
@@ -734,7 +778,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
         if constexpr (POST) {
-            float2 tu = bn_block_sum2(make_float2(t1.x + t1.y, t2.x + t2.y), red, turn);
+            float2 tu = bn_block_sum2(make_float2(t1.x + t1.y, t2.x + t2.y), sh, turn);
             tu = make_float2(p.rms ? 0.f : tu.x * per, tu.y * per);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -746,8 +790,8 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
                 bn_store8(du + k * step, o, true);
             }
         }
-        dx += d;
-        if (du) du += d;
+        dx += hop;
+        if (du) du += hop;
     }
     cp_async_wait_all();
     if (!p.part) return;

@@ -98,13 +98,16 @@ int launch_rows(const BlockNormParams& k, const Shape& s, bimamba_dtype_t ts, bi
 
 constexpr size_t kMaxRunSmem = 200 * 1024;
 
+int run_threads(int d, int k) { return ((d / 8 + k - 1) / k + 31) / 32 * 32; }
+
 // The copying form: 32 to 512 threads of K = 1 or 2 groups of eight columns.
-// False where the copies ahead would not fit (two stages of wide fp32 rows).
+// False where the copies ahead would not fit (wide fp32 rows in the backward).
 template <bool BWD, typename TS, typename TU, int K>
 bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     constexpr int pieces = BWD ? bimamba::kBnBwdPieces<TS, TU, K> : bimamba::kBnFwdPieces<TS, TU, K>;
-    const int threads = ((k.d / 8 + K - 1) / K + 31) / 32 * 32;
-    const size_t smem = (size_t)bimamba::kBnStages<K> * pieces * threads * 16;
+    constexpr int stages = BWD ? bimamba::kBnBwdStages<K> : bimamba::kBnFwdStages<TS, TU>;
+    const int threads = run_threads(k.d, K);
+    const size_t smem = (size_t)stages * pieces * threads * 16;
     if (smem > kMaxRunSmem) return false;
     void (*fn)(BlockNormParams);
     if constexpr (BWD)
@@ -116,8 +119,7 @@ bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     // one limit for all widths: it is raised once a kernel
     if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), kMaxRunSmem))) return true;
     if (!BWD) {  // one run a block that an SM holds
-        const int by_regs = 65536 / (bimamba::kBnFwdRegs * threads);
-        const int held = (int)std::min<size_t>(std::min(by_regs, 24), 220 * 1024 / (smem + 2048));
+        const int held = (int)std::min<size_t>(std::min(512 / threads, 16), 220 * 1024 / (smem + 2048));
         k.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(k.L, (int64_t)kSms * std::max(held, 1) / k.batch));
     }
     fn<<<dim3((unsigned)k.nseg, (unsigned)k.batch), threads, smem, st>>>(k);
@@ -125,10 +127,13 @@ bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     return true;
 }
 
+// Groups of eight columns a thread.  The forward holds two where that leaves
+// two warps a row: half the row sums' work (d 2048 bf16 <<FIGS>>).  The
+// backward's column sums leave room for one, up to 512 threads.
 template <bool BWD, typename TS, typename TU>
 bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
-    return k.d <= 8 * bimamba::kBlockNormThreads ? launch_run_k<BWD, TS, TU, 1>(k, st, rc)
-                                                 : launch_run_k<BWD, TS, TU, 2>(k, st, rc);
+    const bool one = BWD ? k.d <= 8 * bimamba::kBlockNormThreads : k.d < 1024;
+    return one ? launch_run_k<BWD, TS, TU, 1>(k, st, rc) : launch_run_k<BWD, TS, TU, 2>(k, st, rc);
 }
 
 template <bool BWD>
