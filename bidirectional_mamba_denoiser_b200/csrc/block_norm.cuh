@@ -380,10 +380,10 @@ __device__ __forceinline__ Bn8 bn_store8(__nv_bfloat16* p, const Bn8& a, bool st
     return bn_unpack(q);
 }
 __device__ __forceinline__ Bn8 bn_store8(float* p, const Bn8& a, bool store) {
-    if (store) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
-        reinterpret_cast<float4*>(p)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
-    }
+    if (store)  // 32 bytes at once: two halves would write every sector in two parts
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.v[0].x), "f"(a.v[0].y),
+                     "f"(a.v[1].x), "f"(a.v[1].y), "f"(a.v[2].x), "f"(a.v[2].y), "f"(a.v[3].x), "f"(a.v[3].y)
+                     : "memory");
     return a;
 }
 __device__ __forceinline__ Bn8 bn_load8(const float* p, float other) {
@@ -438,32 +438,41 @@ __device__ __forceinline__ float2 bn_block_sum2(float2 v, BnShared& sh, int& tur
 template <typename T>
 constexpr int kBnPieces = (int)sizeof(T) / 2;
 
-// A thread's eight columns of a row into its pieces of a stage, and back.
-// Piece q of thread t is at stage + (q * blockDim.x + t) * 16.
+// A warp's 256 columns of a row, in its part of piece q of a stage, and a
+// lane's eight of them back.  bf16: each lane copies its own 16 bytes.  fp32:
+// lane l copies the chunks l and l + 32 of the warp's 64, so that a copy's
+// sectors are whole; chunk c goes to place c ^ (c / 8 & 1), which spreads a
+// read of 32 bytes a lane over all banks.  (So a warp's copies are waited for,
+// and its reads finished, by the whole warp.)
+__device__ __forceinline__ int bn_place(int c) { return c ^ (c >> 3 & 1); }
 template <typename T>
-__device__ __forceinline__ void bn_fetch(unsigned char* mine, int q, const T* row) {
+__device__ __forceinline__ void bn_fetch(unsigned char* stage, int q, const T* row, int c0, int d) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned char* to = stage + (q * blockDim.x + warp * 32 * kBnPieces<T>) * 16;
 #pragma unroll
-    for (int h = 0; h < kBnPieces<T>; ++h)
-        cp_async<16>(mine + (q + h) * blockDim.x * 16, reinterpret_cast<const char*>(row) + 16 * h, true);
+    for (int h = 0; h < kBnPieces<T>; ++h) {
+        const int c = lane + 32 * h, col = c0 + c * (16 / (int)sizeof(T));
+        if (col < d) cp_async<16>(to + (sizeof(T) == 2 ? c : bn_place(c)) * 16, row + col, true);
+    }
 }
 template <typename T>
-__device__ __forceinline__ Bn8 bn_fetched(const unsigned char* mine, int q) {
+__device__ __forceinline__ Bn8 bn_fetched(const unsigned char* stage, int q) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned char* from = stage + (q * blockDim.x + warp * 32 * kBnPieces<T>) * 16;
     if constexpr (sizeof(T) == 2) {
-        return bn_unpack(*reinterpret_cast<const uint4*>(mine + q * blockDim.x * 16));
+        return bn_unpack(*reinterpret_cast<const uint4*>(from + lane * 16));
     } else {
-        const float4 a = *reinterpret_cast<const float4*>(mine + q * blockDim.x * 16);
-        const float4 b = *reinterpret_cast<const float4*>(mine + (q + 1) * blockDim.x * 16);
+        const float4 a = *reinterpret_cast<const float4*>(from + bn_place(2 * lane) * 16);
+        const float4 b = *reinterpret_cast<const float4*>(from + bn_place(2 * lane + 1) * 16);
         return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
     }
 }
 
-// Zeros in the pieces of a thread that no copy fills: all of a group past the
-// last column, and from piece `from` on without `more`.
-template <int K, int NS, int PER>
-__device__ __forceinline__ void bn_clear(unsigned char* mine, const bool (&in)[K], bool more, int from) {
-    for (int q = 0; q < NS * K * PER; ++q)
-        if (!in[q / PER % K] || (!more && q % PER >= from))
-            *reinterpret_cast<uint4*>(mine + q * blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
+// The block's stages start as zeros: what no copy fills (columns past d, an
+// absent tensor) reads as that.
+__device__ __forceinline__ void bn_clear(unsigned char* smem, int bytes) {
+    for (int q = threadIdx.x * 16; q < bytes; q += blockDim.x * 16) *reinterpret_cast<uint4*>(smem + q) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
 }
 
 // Vectors of a thread's columns: held in registers, or (where there are too
@@ -572,22 +581,20 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_run_kernel(c
     // rows seg, seg + nseg, ...: the blocks move through memory together
     const int64_t r0 = b * p.L + seg, hop = (int64_t)p.nseg * d;
     const int rows = (int)((p.L - seg + p.nseg - 1) / p.nseg);
-    unsigned char* const mine = bn_smem + threadIdx.x * 16;
     const int stage_bytes = PIECES * blockDim.x * 16;
-    const TS* x_in = static_cast<const TS*>(p.x) + r0 * d + col0;   // the next row to copy
-    const TU* u_in = p.u ? static_cast<const TU*>(p.u) + r0 * d + col0 : nullptr;
+    const TS* x_in = static_cast<const TS*>(p.x) + r0 * d;   // the next row to copy
+    const TU* u_in = p.u ? static_cast<const TU*>(p.u) + r0 * d : nullptr;
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) in[k] = col0 + k * step < d;
-    // what is never copied (columns past d, an absent branch) reads as zeros
-    bn_clear<K, NS, PS + PU>(mine, in, u_in != nullptr, PS);
+    const int warp_col = (threadIdx.x >> 5) * 256;
+    if (d != K * step || !p.u) bn_clear(bn_smem, NS * stage_bytes);
     auto fetch = [&](int row, int s) {
         if (row < rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (!in[k]) continue;
-                bn_fetch(mine + s * stage_bytes, k * (PS + PU), x_in + k * step);
-                if (u_in) bn_fetch(mine + s * stage_bytes, k * (PS + PU) + PS, u_in + k * step);
+                bn_fetch(bn_smem + s * stage_bytes, k * (PS + PU), x_in, warp_col + k * step, d);
+                if (u_in) bn_fetch(bn_smem + s * stage_bytes, k * (PS + PU) + PS, u_in, warp_col + k * step, d);
             }
             x_in += hop;
             if (u_in) u_in += hop;
@@ -608,8 +615,9 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_run_kernel(c
     TU* y = p.y ? static_cast<TU*>(p.y) + r0 * d + col0 : nullptr;
     int s = 0;
     for (int row = 0; row < rows; ++row) {
-        unsigned char* const stage = mine + s * stage_bytes;
+        const unsigned char* const stage = bn_smem + s * stage_bytes;
         cp_async_wait_pending<NS - 1>();
+        __syncwarp();
         Bn8 x[K], u[K];
         float2 sx = make_float2(0.f, 1.f), su = make_float2(0.f, 1.f);
 #pragma unroll
@@ -617,6 +625,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_run_kernel(c
             x[k] = bn_fetched<TS>(stage, k * (PS + PU));
             u[k] = bn_fetched<TU>(stage, k * (PS + PU) + PS);
         }
+        __syncwarp();
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
         if constexpr (POST) su = bn_row_stats<K>(u, in, p, own_inv, sh, turn);
@@ -665,23 +674,21 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     // rows seg, seg + nseg, ...: the blocks move through memory together
     const int64_t r0 = b * p.L + seg, hop = (int64_t)p.nseg * d;
     const int rows = (int)((p.L - seg + p.nseg - 1) / p.nseg);
-    unsigned char* const mine = bn_smem + threadIdx.x * 16;
+    const int warp_col = (threadIdx.x >> 5) * 256;
     const int stage_bytes = PIECES * blockDim.x * 16;
-    int64_t at = r0 * d + col0;  // the next row to copy
+    int64_t at = r0 * d;  // the next row to copy
     auto fetch = [&](int row, int s) {
         if (row < rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int q = k * 2 * (PS + PU);
-                if (col0 + k * step >= d) continue;
-                const int64_t c = at + k * step;
-                unsigned char* const stage = mine + s * stage_bytes;
+                const int q = k * 2 * (PS + PU), c = warp_col + k * step;
+                unsigned char* const stage = bn_smem + s * stage_bytes;
                 if (p.dy) {
-                    bn_fetch(stage, q, static_cast<const TS*>(p.x) + c);
-                    bn_fetch(stage, q + PS, static_cast<const TU*>(p.dy) + c);
+                    bn_fetch(stage, q, static_cast<const TS*>(p.x) + at, c, d);
+                    bn_fetch(stage, q + PS, static_cast<const TU*>(p.dy) + at, c, d);
                 }
-                if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + c);
-                if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + c);
+                if (p.dx_out) bn_fetch(stage, q + PS + PU, static_cast<const TS*>(p.dx_out) + at, c, d);
+                if (p.u) bn_fetch(stage, q + 2 * PS + PU, static_cast<const TU*>(p.u) + at, c, d);
             }
             at += hop;
         }
@@ -705,10 +712,11 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     float4 ahead = rows > 0 ? stats[0] : make_float4(0.f, 0.f, 0.f, 0.f);
     int s = 0;
     for (int row = 0; row < rows; ++row) {
-        unsigned char* const stage = mine + s * stage_bytes;
+        const unsigned char* const stage = bn_smem + s * stage_bytes;
         const float4 st = ahead;
         if (row + 1 < rows) ahead = stats[(int64_t)(row + 1) * p.nseg];
         cp_async_wait_pending<NS - 1>();
+        __syncwarp();
         Bn8 n[K], dy[K], D[K];
         float2 sum = bn_f2(0.f);
         if (p.dy) {
@@ -775,6 +783,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
                 bn_store8(du + k * step, o, true);
             }
         }
+        __syncwarp();
         fetch(row + NS, s);
         s = s + 1 == NS ? 0 : s + 1;
         if constexpr (POST) {

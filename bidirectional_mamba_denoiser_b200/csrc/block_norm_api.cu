@@ -138,7 +138,10 @@ bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
 
 template <bool BWD>
 int launch(BlockNormParams& k, bool vec, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
-    if (vec && k.d >= 256 && k.d <= 16 * bimamba::kBlockNormThreads) {  // narrower rows would not fill a warp
+    // its fp32 stores are of 32 bytes
+    const bool wide = (ts == BIMAMBA_BF16 || (aligned(k.x_out, 32) && aligned(k.dx, 32))) &&
+                      (tu == BIMAMBA_BF16 || (aligned(k.y, 32) && aligned(k.du, 32)));
+    if (vec && wide && k.d >= 256 && k.d <= 16 * bimamba::kBlockNormThreads) {  // narrower rows would not fill a warp
         int rc = BIMAMBA_OK;
         if (ts == BIMAMBA_BF16 ? launch_run<BWD, bf16, bf16>(k, st, rc)
                                : (tu == BIMAMBA_BF16 ? launch_run<BWD, float, bf16>(k, st, rc)
