@@ -9,7 +9,9 @@ there is no other implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -156,18 +158,16 @@ def _load():
     lib.bimamba2_block_step.restype = I
     lib.bimamba_glr_workspace_bytes.argtypes = [I, I64, I, I]
     lib.bimamba_glr_workspace_bytes.restype = SZ
-    lib.bimamba_glr_fwd.argtypes = [ctypes.POINTER(GlrInputs), ctypes.POINTER(GlrParams), P, ctypes.POINTER(Rows),
-                                    P, P, I, I64, I, U, P, SZ, P]
+    # (structures as packed bytes: building ctypes objects would cost a short call more than its kernel)
+    lib.bimamba_glr_fwd.argtypes = [P, P, P, P, P, P, I, I64, I, U, P, SZ, P]
     lib.bimamba_glr_fwd.restype = I
-    lib.bimamba_glr_bwd.argtypes = [ctypes.POINTER(GlrInputs), ctypes.POINTER(GlrParams), ctypes.POINTER(Rows),
-                                    P, P, ctypes.POINTER(GlrGrads), I, I64, I, U, P, SZ, P]
+    lib.bimamba_glr_bwd.argtypes = [P, P, P, P, P, P, I, I64, I, U, P, SZ, P]
     lib.bimamba_glr_bwd.restype = I
-    lib.bimamba_block_norm_fwd.argtypes = [P, P, ctypes.POINTER(BlockNormParams), P, P, P, I, I, I, I64, I, U, P]
+    lib.bimamba_block_norm_fwd.argtypes = [P, P, P, P, P, P, I, I, I, I64, I, U, P]
     lib.bimamba_block_norm_fwd.restype = I
     lib.bimamba_block_norm_workspace_bytes.argtypes = [I, I64, I]
     lib.bimamba_block_norm_workspace_bytes.restype = SZ
-    lib.bimamba_block_norm_bwd.argtypes = [P, P, P, P, P, ctypes.POINTER(BlockNormParams),
-                                           ctypes.POINTER(BlockNormGrads), I, I, I, I64, I, U, P, SZ, P]
+    lib.bimamba_block_norm_bwd.argtypes = [P, P, P, P, P, P, P, I, I, I, I64, I, U, P, SZ, P]
     lib.bimamba_block_norm_bwd.restype = I
     lib.bimamba_features.argtypes = [ctypes.POINTER(Inputs), ctypes.POINTER(Params), I, I64, I, P, P, P]
     lib.bimamba_features.restype = I
@@ -562,26 +562,49 @@ def bimamba2_block_step(state, xbc, z, dt, params: dict, out=None, out_dtype=Non
 
 # ---------------------------------------------------------------- gated linear recurrence
 
+# The structures above, packed (native alignment): rows, a call's inputs,
+# parameters and gradients.
+_ROWS = struct.Struct("Pqq")
+_GLR_INPUTS = struct.Struct("Pqq" * 5 + "Pi0P")
+_GLR_PARAMS = struct.Struct("PPP")
+_GLR_GRADS = struct.Struct("Pqq" * 5 + "PPPP")
+_NORM_PARAMS = struct.Struct("PPPPff")
+_NORM_GRADS = struct.Struct("PPPPPP")
+_NO_ROWS = (0, 0, 0)
+
+
 def _check(t, name: str, shape, dtype, device):
-    """`t` (or None) must have this shape and dtype and lie on `device`."""
-    if t is None:
+    """`t` (or None) must have this shape and dtype and lie on `device` (a GPU)."""
+    if t is None or (t.dtype == dtype and t.shape == shape and t.device == device):
         return
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
-def _rows(t, name: str) -> Rows:
-    """[b, L, D] with contiguous channels (any batch and token strides)."""
+def _rows(t, name: str):
+    """[b, L, D] with contiguous channels (any batch and token strides): pointer and strides."""
     if t is None:
-        return Rows(None, 0, 0)
+        return _NO_ROWS
     sb, sl, sd = t.stride()
     if sd != 1 and t.shape[2] != 1:
         raise ValueError(f"{name} must have contiguous channels (stride 1 in its last dimension)")
-    return Rows(t.data_ptr(), sb, sl)
+    return t.data_ptr(), sb, sl
+
+
+def _vec(t, name: str, shape, device) -> int:
+    """The address of a contiguous fp32 tensor of this shape (0 for None)."""
+    if t is None:
+        return 0
+    _check(t, name, shape, torch.float32, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (of a Stream object would take 2 us)
 
 
 class _On:
@@ -599,7 +622,7 @@ class _On:
         else:
             if torch.cuda.current_device() != device.index:
                 self._ctx = torch.cuda.device(device)
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.handle = _raw_stream(device.index)
 
     def __enter__(self):
         if self._ctx is not None:
@@ -620,23 +643,27 @@ def _workspace_for(workspace, need: int, device):
     return workspace
 
 
+@functools.lru_cache(maxsize=256)
 def bimamba_glr_workspace_bytes(batch: int, L: int, d_inner: int, backward: bool = False) -> int:
     return int(lib.bimamba_glr_workspace_bytes(batch, L, d_inner, 1 if backward else 0))
 
 
 def _glr_inputs(x, r, i, params: dict, add, z, lengths):
-    b, L, D = x.shape
-    dev = x.device
-    code = _dtype_code(x.dtype)
+    b, L, D = shape = x.shape
+    dev, dtype = x.device, x.dtype
+    code = _dtype_code(dtype)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     for t, name in ((r, "r"), (i, "i"), (add, "add"), (z, "z")):
-        _check(t, name, x.shape, x.dtype, dev)
-    _check(lengths, "lengths", (b,), torch.int32, dev)
-    for name in ("A", "r_bias", "i_bias"):
-        _check(params.get(name), name, (D,), torch.float32, dev)
-    inp = GlrInputs(_rows(x, "x"), _rows(r, "r"), _rows(i, "i"), _rows(add, "add"), _rows(z, "z"), _ptr(lengths), code)
-    return inp, GlrParams(_ptr(params["A"]), _ptr(params.get("r_bias")), _ptr(params.get("i_bias")))
+        _check(t, name, shape, dtype, dev)
+    if lengths is not None:
+        _check(lengths, "lengths", (b,), torch.int32, dev)
+    inp = _GLR_INPUTS.pack(*_rows(x, "x"), *_rows(r, "r"), *_rows(i, "i"), *_rows(add, "add"), *_rows(z, "z"),
+                           _ptr(lengths) or 0, code)
+    get, vec = params.get, (D,)
+    par = _GLR_PARAMS.pack(_vec(params["A"], "A", vec, dev), _vec(get("r_bias"), "r_bias", vec, dev),
+                           _vec(get("i_bias"), "i_bias", vec, dev))
+    return inp, par
 
 
 def bimamba_glr_fwd(x, r, i, params: dict, reverse: bool = False, add=None, z=None, lengths=None, h_in=None,
@@ -651,18 +678,19 @@ def bimamba_glr_fwd(x, r, i, params: dict, reverse: bool = False, add=None, z=No
     b, L, D = x.shape
     dev = x.device
     inp, par = _glr_inputs(x, r, i, params, add, z, lengths)
-    _check(h_in, "h_in", (b, D), torch.float32, dev)
-    _check(h_out, "h_out", (b, D), torch.float32, dev)
-    _check(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), torch.float32, dev)
+    row = (b, D)
+    h0, h1 = _vec(h_in, "h_in", row, dev), _vec(h_out, "h_out", row, dev)
+    saved = _vec(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), dev)
     _check(out, "out", x.shape, x.dtype, dev)
     with _On(dev, stream) as on:
         if out is None:
-            out = torch.empty(b, L, D, device=dev, dtype=x.dtype)
-        workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D), dev)
-        rc = lib.bimamba_glr_fwd(ctypes.byref(inp), ctypes.byref(par), _ptr(h_in), ctypes.byref(_rows(out, "out")),
-                                 _ptr(h_out), _ptr(chunk_states), b, L, D,
-                                 flags | (BIMAMBA_GLR_REVERSE if reverse else 0), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), on.handle)
+            out = torch.empty((b, L, D), device=dev, dtype=x.dtype)
+        ws, ws_bytes = 0, 0
+        if L > GLR_CHUNK or workspace is not None:  # a shorter call needs none
+            workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D), dev)
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        rc = lib.bimamba_glr_fwd(inp, par, h0, _ROWS.pack(*_rows(out, "out")), h1, saved, b, L, D,
+                                 flags | BIMAMBA_GLR_REVERSE if reverse else flags, ws, ws_bytes, on.handle)
     if rc != BIMAMBA_OK:
         raise BimambaError("bimamba_glr_fwd", rc)
     return out
@@ -680,9 +708,8 @@ def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = F
     dev = x.device
     inp, par = _glr_inputs(x, r, i, params, add, z, lengths)
     _check(dout, "dout", x.shape, x.dtype, dev)
-    _check(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), torch.float32, dev)
-    _check(dh_out, "dh_out", (b, D), torch.float32, dev)
-    _check(dh_in, "dh_in", (b, D), torch.float32, dev)
+    saved = _vec(chunk_states, "chunk_states", (b, (L + GLR_CHUNK - 1) // GLR_CHUNK, D), dev)
+    g_out, g_in = _vec(dh_out, "dh_out", (b, D), dev), _vec(dh_in, "dh_in", (b, D), dev)
     for t, name in ((dx, "dx"), (dr, "dr"), (di, "di")):
         _check(t, name, x.shape, x.dtype, dev)
     with _On(dev, stream) as on:
@@ -697,12 +724,12 @@ def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = F
         for name in ("A", "r_bias", "i_bias"):
             if params.get(name) is not None:
                 res["d" + name] = torch.empty(D, device=dev, dtype=torch.float32)
-        g = GlrGrads(*(_rows(res.get(k), k) for k in ("dx", "dr", "di", "dadd", "dz")),
-                     *(_ptr(res.get(k)) for k in ("dA", "dr_bias", "di_bias")), _ptr(dh_in))
+        grads = [v for k in ("dx", "dr", "di", "dadd", "dz") for v in _rows(res.get(k), k)]
+        sums = [res[k].data_ptr() if k in res else 0 for k in ("dA", "dr_bias", "di_bias")]
         workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D, True), dev)
-        rc = lib.bimamba_glr_bwd(ctypes.byref(inp), ctypes.byref(par), ctypes.byref(_rows(dout, "dout")),
-                                 _ptr(chunk_states), _ptr(dh_out), ctypes.byref(g), b, L, D,
-                                 flags | (BIMAMBA_GLR_REVERSE if reverse else 0), _ptr(workspace),
+        rc = lib.bimamba_glr_bwd(inp, par, _ROWS.pack(*_rows(dout, "dout")), saved, g_out,
+                                 _GLR_GRADS.pack(*grads, *sums, g_in), b, L, D,
+                                 flags | BIMAMBA_GLR_REVERSE if reverse else flags, workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), on.handle)
     if rc != BIMAMBA_OK:
         raise BimambaError("bimamba_glr_bwd", rc)
@@ -713,18 +740,19 @@ def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = F
 
 def _block_norm_params(b: int, d: int, dev, gate, post_w, gamma, beta, res_scale, eps, rms):
     flags = BIMAMBA_NORM_RMS if rms else 0
-    if gate is not None:
-        shared = gate.dim() == 1
-        _check(gate, "gate", (d,) if shared else (b, d), torch.float32, dev)
-        flags |= BIMAMBA_NORM_GATE_SHARED if shared else 0
-    _check(post_w, "post_w", (d,), torch.float32, dev)
-    one = gamma if gamma is not None else beta
-    if one is not None:
-        shape = (d,) if one.dim() == 1 else (b, d)
-        _check(gamma, "gamma", shape, torch.float32, dev)
-        _check(beta, "beta", shape, torch.float32, dev)
-        flags |= BIMAMBA_NORM_GAMMA_SHARED if one.dim() == 1 else 0
-    return BlockNormParams(_ptr(gate), _ptr(post_w), _ptr(gamma), _ptr(beta), res_scale, eps), flags
+    each, one = (b, d), (d,)
+    g_shape = gamma_shape = each
+    if gate is not None and gate.dim() == 1:
+        flags |= BIMAMBA_NORM_GATE_SHARED
+        g_shape = one
+    first = gamma if gamma is not None else beta
+    if first is not None and first.dim() == 1:
+        flags |= BIMAMBA_NORM_GAMMA_SHARED
+        gamma_shape = one
+    par = _NORM_PARAMS.pack(_vec(gate, "gate", g_shape, dev), _vec(post_w, "post_w", one, dev),
+                            _vec(gamma, "gamma", gamma_shape, dev), _vec(beta, "beta", gamma_shape, dev),
+                            res_scale, eps)
+    return par, flags
 
 
 def bimamba_block_norm_fwd(x, u=None, gate=None, post_w=None, gamma=None, beta=None, res_scale: float = 1.0,
@@ -745,17 +773,17 @@ def bimamba_block_norm_fwd(x, u=None, gate=None, post_w=None, gamma=None, beta=N
     ty = u.dtype if u is not None else (dtype or x.dtype)
     par, flags = _block_norm_params(b, d, dev, gate, post_w, gamma, beta, res_scale, eps, rms)
     _check(u, "u", x.shape, ty, dev)
-    _check(stats, "stats", (b, L, 4), torch.float32, dev)
+    saved = _vec(stats, "stats", (b, L, 4), dev)
     _check(x_out, "x_out", x.shape, x.dtype, dev)
     _check(y, "y", x.shape, ty, dev)
     with _On(dev, stream) as on:
         stored = x_out
         if stored is None and (u is not None or res_scale != 1.0):
-            stored = torch.empty_like(x, memory_format=torch.contiguous_format)
+            stored = torch.empty((b, L, d), device=dev, dtype=x.dtype)
         if y is None and norm:
-            y = torch.empty(b, L, d, device=dev, dtype=ty)
-        rc = lib.bimamba_block_norm_fwd(_ptr(x), _ptr(u), ctypes.byref(par), _ptr(stored), _ptr(y if norm else None),
-                                        _ptr(stats), _dtype_code(x.dtype), _dtype_code(ty), b, L, d, flags, on.handle)
+            y = torch.empty((b, L, d), device=dev, dtype=ty)
+        rc = lib.bimamba_block_norm_fwd(_ptr(x), _ptr(u), par, _ptr(stored), _ptr(y if norm else None),
+                                        saved, _dtype_code(x.dtype), _dtype_code(ty), b, L, d, flags, on.handle)
     if rc != BIMAMBA_OK:
         raise BimambaError("bimamba_block_norm_fwd", rc)
     return (x if stored is None else stored), (y if norm else None)
@@ -805,10 +833,10 @@ def bimamba_block_norm_bwd(dy, dx_out, x_out, stats, u=None, gate=None, post_w=N
             res["dgamma"] = vec(gamma.shape)
         if want_dbeta and dy is not None:
             res["dbeta"] = vec((d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d))
-        g = BlockNormGrads(*(_ptr(res.get(k)) for k in ("dx", "du", "dgate", "dpost_w", "dgamma", "dbeta")))
+        g = _NORM_GRADS.pack(*(_ptr(res.get(k)) or 0 for k in ("dx", "du", "dgate", "dpost_w", "dgamma", "dbeta")))
         workspace = _workspace_for(workspace, bimamba_block_norm_workspace_bytes(b, L, d), dev)
-        rc = lib.bimamba_block_norm_bwd(_ptr(dy), _ptr(dx_out), _ptr(x_out), _ptr(u), _ptr(stats), ctypes.byref(par),
-                                        ctypes.byref(g), _dtype_code(x_out.dtype), _dtype_code(ty), b, L, d, flags,
+        rc = lib.bimamba_block_norm_bwd(_ptr(dy), _ptr(dx_out), _ptr(x_out), _ptr(u), _ptr(stats), par,
+                                        g, _dtype_code(x_out.dtype), _dtype_code(ty), b, L, d, flags,
                                         _ptr(workspace), workspace.numel() * workspace.element_size(), on.handle)
     if rc != BIMAMBA_OK:
         raise BimambaError("bimamba_block_norm_bwd", rc)

@@ -237,7 +237,9 @@ int bimamba_glr_fwd(const bimamba_glr_inputs_t* in, const bimamba_glr_params_t* 
     if (!out) return BIMAMBA_ERR_INVALID_ARG;
     if ((rc = check_out(*out, elem_size(in->dtype), batch, L, d_inner))) return rc;
     if (!aligned(h_in, 4) || !aligned(h_out, 4) || !aligned(chunk_states, 4)) return BIMAMBA_ERR_MISALIGNED;
-    if ((rc = check_workspace(workspace, workspace_bytes, bimamba_glr_workspace_bytes(batch, L, d_inner, 0)))) return rc;
+    if (L > BIMAMBA_GLR_CHUNK &&
+        (rc = check_workspace(workspace, workspace_bytes, bimamba_glr_workspace_bytes(batch, L, d_inner, 0))))
+        return rc;
 
     GlrParams k = {};
     fill_common(k, in, p, batch, L, d_inner, flags);

@@ -484,7 +484,8 @@ size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backwa
  *                entering each BIMAMBA_GLR_CHUNK steps, which bimamba_glr_bwd needs
  *                (chunks that start at or after len are left as they were)
  *   workspace    >= bimamba_glr_workspace_bytes(..., 0) bytes, 256-byte aligned
- *                (two calls that overlap on the GPU need one each)
+ *                (two calls that overlap on the GPU need one each); not looked at, and
+ *                may be NULL, for L <= BIMAMBA_GLR_CHUNK
  * flags: BIMAMBA_GLR_REVERSE. */
 int bimamba_glr_fwd(const bimamba_glr_inputs_t *in, const bimamba_glr_params_t *p, const float *h_in,
                     const bimamba_rows_t *out, float *h_out, float *chunk_states,
