@@ -238,15 +238,17 @@ constexpr unsigned kGlrErrTimeout = 4u;  // a wait for an earlier tile gave up
 
 static __device__ unsigned int g_glr_error;
 
-constexpr int kGlrGone = 32;  // a line of its own
+constexpr int kGlrPad = 16, kGlrGone = 32;  // other sectors
 
 struct GlrSync {
-    unsigned int* ticket;        // [0] the tickets, [kGlrGone] zero once a wait ran out; all ones before the
+    unsigned int* ticket;        // [0] the tickets, [kGlrPad] those of glr_pad, [kGlrGone] zero once a wait ran out; all ones before the
                                  // launch.  Null: one tile a row, nothing to hand over
     unsigned long long* map;     // [batch * slabs][tiles][64]: (P, h) of each channel
     float* state;                // [batch * slabs][groups][64]: state entering each group
     int64_t tiles, groups;
     unsigned total;              // tiles of all rows and slabs
+    int4* plan;                  // padded batches with a hand-over: [0] {count}, then the tiles that have steps in
+                                 // ticket order, {at, row, length}; else null
     long long wait_limit;
     int starve;                  // test aid: publish nothing
 };
@@ -280,6 +282,13 @@ __device__ __forceinline__ GlrTile glr_tile(const GlrParams& p, const GlrSync& y
     if (id >= y.total) return {-1, 0, 0, 0};
     const unsigned slabs = glr_slabs(p), chains = slabs * (unsigned)p.batch;
     GlrTile t;
+    if (y.plan) {
+        const int4 e = y.plan[1 + id / slabs];  // (in range: id < total)
+        if (id / slabs >= (unsigned)y.plan[0].x) return {-1, 0, 0, 0};
+        t.at = e.x, t.b = e.y, t.len = e.z;
+        t.rs = t.b * (int)slabs + (int)(id % slabs);
+        return t;
+    }
     t.at = (int)(id / chains);
     t.rs = (int)(id % chains);
     t.b = t.rs / (int)slabs;
@@ -358,13 +367,13 @@ __device__ __forceinline__ float2 glr_through(const float4 (*maps)[32], float2 c
     return c;
 }
 
-// The tile's first step.  BWD: tiles are walked from the row's last to its
-// first, then those past its length.
+// The tile's first step (a row without tokens has one empty tile, or none).
+// BWD: tiles are walked from the row's last to its first.
 template <bool BWD>
 __device__ __forceinline__ int64_t glr_first_step(const GlrTile& t, int tile_steps) {
     if constexpr (!BWD) return (int64_t)t.at * tile_steps;
-    const int64_t used = ((int64_t)t.len + tile_steps - 1) / tile_steps;
-    return (t.at < used ? used - 1 - t.at : t.at) * tile_steps;
+    const int64_t used = t.len > 0 ? ((int64_t)t.len + tile_steps - 1) / tile_steps : 1;
+    return (used - 1 - t.at) * tile_steps;
 }
 
 // The tiles of a block, in shared memory, a few ahead, each with the byte
@@ -409,15 +418,88 @@ struct GlrQueue {
     }
 };
 
-// The rest of a row behind its length: zeros from token t0 up to t1.
-template <typename T, bool VEC>
-__device__ __forceinline__ void glr_zero_rows(const GlrParams& p, int tensor, int64_t b, int64_t t0, int64_t t1, int c0,
-                                              int nch) {
-    const GlrRows& q = p.rows[tensor];
-    if (!q.p) return;
-    for (int64_t t = t0 + (threadIdx.x >> 5); t < t1; t += blockDim.x >> 5)
-        glr_st2<VEC>(reinterpret_cast<T*>(q.p + b * q.bs + t * (q.ts < 0 ? -(int64_t)q.ts : q.ts)) + c0,
-                     make_float2(0.f, 0.f), nch);
+// Before the tiles of a padded batch: the hand-over workspace's fill (`bytes`
+// of ones), the states of rows without tokens, and the plan, which lists level
+// by level the rows that have a tile there: before tile `at` of row b stand
+// sum_j min(tiles_j, at) + #{j < b: tiles_j > at}.
+__global__ void __launch_bounds__(256)
+    glr_plan_kernel(const __grid_constant__ GlrParams p, uint4* fill, int64_t bytes, int4* plan, int64_t tiles,
+                    int tile_steps) {
+    __shared__ int before, count;
+    for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < bytes / 16; k += (int64_t)gridDim.x * blockDim.x)
+        fill[k] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int64_t item = blockIdx.x; item < p.batch * tiles; item += gridDim.x) {
+        const int64_t b = item / tiles, len = glr_len(p, b);
+        const int here = (int)(item % tiles);
+        const bool there = len > (int64_t)here * tile_steps;
+        if (plan && (there || item == 0)) {
+            if (threadIdx.x == 0) before = count = 0;
+            __syncthreads();
+            for (int j = threadIdx.x; j < p.batch; j += blockDim.x) {
+                const int own = (int)((glr_len(p, j) + tile_steps - 1) / tile_steps);
+                atomicAdd(&before, min(own, here) + (j < b && own > here));
+                atomicAdd(&count, own);
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                if (there) plan[1 + before] = make_int4(here, (int)b, (int)len, 0);
+                if (item == 0) plan[0] = make_int4(count, 0, 0, 0);
+            }
+            __syncthreads();
+        }
+        if (here == 0 && len == 0) {
+            const float* from = p.part ? p.dh_out : p.h_in;
+            float* to = p.part ? p.dh_in : p.h_out;
+            if (to)
+                for (int64_t k = threadIdx.x; k < p.D; k += blockDim.x) to[b * p.D + k] = from ? from[b * p.D + k] : 0.f;
+        }
+    }
+}
+
+// Zeros behind a padded row's length, kGlrPadTokens of one row at a time
+// (`item` counts them), in every output and in the backward's partial sums: the
+// work of blocks that find no more tiles, while the last chains still run.
+constexpr int kGlrPadTokens = 16;
+template <typename T>
+__device__ __noinline__ void glr_pad_rows(const GlrParams& p, int64_t item) {
+    const int64_t per_row = (p.L + kGlrPadTokens - 1) / kGlrPadTokens;
+    const int64_t b = item / per_row, s0 = item % per_row * kGlrPadTokens, len = glr_len(p, b);
+    const int64_t t0 = len > s0 ? len : s0, t1 = s0 + kGlrPadTokens < p.L ? s0 + kGlrPadTokens : p.L;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+    for (int q = kGlrOut; q < kGlrTensors; ++q) {
+        const GlrRows& r = p.rows[q];
+        if (!r.p) continue;
+        const int64_t ts = r.ts < 0 ? -(int64_t)r.ts : r.ts;
+        const bool wide = p.D * sizeof(T) % 16 == 0 && (reinterpret_cast<uintptr_t>(r.p) | r.bs | ts) % 16 == 0;
+        for (int64_t t = t0 + warp; t < t1; t += nwarp) {
+            char* const to = r.p + b * r.bs + t * ts;
+            if (wide) {
+                for (int k = lane; k < p.D / (16 / (int)sizeof(T)); k += 32)
+                    reinterpret_cast<uint4*>(to)[k] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                for (int k = lane; k < p.D; k += 32) reinterpret_cast<T*>(to)[k] = T(0.f);
+            }
+        }
+    }
+    if (p.part && len <= s0 && s0 % kGlrChunk == 0) {
+        float* const part = p.part + (b * p.nchunk + s0 / kGlrChunk) * 3 * p.D;
+        for (int64_t k = threadIdx.x; k < 3LL * p.D; k += blockDim.x) part[k] = 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void glr_pad(const GlrParams& p, const GlrSync& y, unsigned* slot) {
+    const int64_t items = p.batch * ((p.L + kGlrPadTokens - 1) / kGlrPadTokens);
+    __syncthreads();
+    for (int64_t k = blockIdx.x;; k += gridDim.x) {
+        if (y.ticket) {
+            if (threadIdx.x == 0) *slot = atomicAdd(y.ticket + kGlrPad, 1u) + 1u;
+            __syncthreads();
+            k = *slot;
+            __syncthreads();
+        }
+        if (k >= items) break;
+        glr_pad_rows<T>(p, k);
+    }
 }
 // Steps of a row of `len` that start at ws, at most `most`.
 __device__ __forceinline__ int glr_steps(int64_t len, int64_t ws, int most) {
@@ -547,13 +629,8 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const int64_t s0 = (int64_t)t.at * tile_steps, s1 = s0 + tile_steps;  // the tile's steps [s0, s1)
         const int64_t ws = s0 + warp * TOK, row = (int64_t)t.b * p.D + c0;
         const int n = glr_steps(t.len, ws, TOK);
-        const bool active = t.len > s0;
-        if (t.len < s1)
-            glr_zero_rows<T, VEC>(p, kGlrOut, t.b, t.len > s0 ? t.len : s0, s1 < p.L ? s1 : p.L, c0, nch);
-        if (t.len == 0 && t.at == 0 && warp == 0 && p.h_out)
-            glr_st2<VEC>(p.h_out + row, glr_vec2<VEC>(p.h_in, row, nch), nch);
         GlrPiece piece;
-        if (active && t.at) glr_ask(piece, y, t, warp);
+        if (t.at) glr_ask(piece, y, t, warp);
         float4(*agg)[32] = aggs[k & 1];
         float4(*got)[32] = pieces[k & 1];
         float2 Ps[TOK], hs[TOK];
@@ -593,10 +670,6 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         __syncthreads();
         t = e.t;  // (read again rather than kept)
-        if (!active) {
-            copy_inputs(queue[(k + NS) % kGlrQueue], stage);
-            continue;
-        }
         const bool last = s1 >= t.len, publish = y.ticket && !last && !y.starve;
         float2 P = glr_f2(1.f), h = glr_f2(0.f);
         if (warp == 0) {
@@ -653,6 +726,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             outputs(std::false_type{});
     }
     cp_async_wait_all();
+    if (p.lengths) glr_pad<T>(p, y, reinterpret_cast<unsigned*>(queue));
 }
 
 // Backward, tiles of kGlrChunk steps: they are walked from the last step to
@@ -729,20 +803,12 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const int64_t s0 = glr_first_step<true>(t, kGlrChunk), s1 = s0 + kGlrChunk, row = (int64_t)t.b * p.D + c0;
         const int64_t chunk = ((int64_t)t.b * p.nchunk + s0 / kGlrChunk) * p.D;
         const int n = glr_steps(t.len, s0 + warp * TOK, TOK);
-        const bool active = t.len > s0;
-        if (t.len < s1) {
-            const int64_t z0 = t.len > s0 ? t.len : s0, z1 = s1 < p.L ? s1 : p.L;
-            for (int q = kGlrDx; q <= kGlrDz; ++q) glr_zero_rows<T, VEC>(p, q, t.b, z0, z1, c0, nch);
-        }
-        if (!active && t.at == 0 && warp == 0 && p.dh_in)
-            glr_st2<VEC>(p.dh_in + row, glr_vec2<VEC>(p.dh_out, row, nch), nch);
         GlrPiece piece;
-        if (active && t.at) glr_ask(piece, y, t, warp);
+        if (t.at) glr_ask(piece, y, t, warp);
         T* in = mine + stage * NT * ROWS;
         const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_z = in + 4 * ROWS, *in_add = in + 5 * ROWS;
         float2 rg[TOK], ig[TOK], u[TOK], hp[TOK];
-        float2 entering = glr_f2(0.f);
-        if (active) entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
+        const float2 entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
         cp_async_wait_pending<NS - 1>();
         __syncwarp();
         float2 P = glr_f2(1.f), q = glr_f2(0.f), h = glr_f2(0.f);
@@ -781,105 +847,101 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         part = p.part + chunk * 3 + c0;
         part_n = nch;
         float2 sA = glr_f2(0.f), sr = glr_f2(0.f), si = glr_f2(0.f);
-        if (active) {
-            const bool last = s0 == 0, publish = y.ticket && !last && !y.starve;
-            // the map from the tile's end to the warp's, and for warp 0 to the tile's start
-            float2 Pw = glr_f2(1.f), qw = glr_f2(0.f);
+        const bool last = s0 == 0, publish = y.ticket && !last && !y.starve;
+        // the map from the tile's end to the warp's, and for warp 0 to the tile's start
+        float2 Pw = glr_f2(1.f), qw = glr_f2(0.f);
 #pragma unroll
-            for (int w = kGlrWarps - 1; w > 0; --w) {
-                const float4 a = agg[w][lane];
-                if (w <= warp) continue;
-                Pw = glr_mul(Pw, make_float2(a.x, a.z));
-                qw = glr_apply(a, qw);
-            }
-            q = glr_fma(P, qw, q);
-            P = glr_mul(P, Pw);
-            if (publish && warp == 0) glr_publish_map(glr_map(y, t, t.at), P, q);
-            float4 mypiece = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t.at) {
-                mypiece = glr_wait_piece(y, piece, t, warp);
-            } else if (warp == kGlrGroup - 1) {
-                const float2 c = glr_vec2<VEC>(p.dh_out, row, nch);
-                mypiece = make_float4(0.f, c.x, 0.f, c.y);
-            }
-            pieces[warp][lane] = mypiece;
-            // the states before the warp's steps, from the one that enters the tile
-            if (n) {
-                float2 c = entering;
-#pragma unroll
-                for (int w = 0; w < kGlrWarps - 1; ++w) {
-                    const float4 a = agg[w][lane];
-                    const float2 hw = aggh[w][lane];
-                    if (w < warp) c = glr_fma(make_float2(a.x, a.z), c, hw);
-                }
-#pragma unroll
-                for (int j = 0; j < TOK; ++j) {
-                    hp[j] = glr_add(c, hp[j]);
-                    c = glr_sub(c, glr_mul(u[j], c));
-                }
-            }
-            __syncthreads();
-            const float4 from = pieces[kGlrGroup - 1][lane];
-            float2 c = make_float2(from.y, from.w);
-            c = glr_through(pieces, c, t.at % kGlrGroup);
-            if (warp == 0) {
-                const float2 end = glr_fma(P, c, q);
-                // the other tiles take the last state's gradient from here, not from dh_out, which may be dh_in
-                if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
-                if (publish && (t.at + 1) % kGlrGroup == 0)
-                    glr_publish_state(glr_state(y, t, t.at + 1), end);
-                if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
-            }
-            q = glr_fma(Pw, c, qw);
-            const float2 A = glr_vec2<VEC>(p.A, c0, nch);
-            // where the warp's steps go, from its last to its first
-            char* to[kGlrDz - kGlrDx + 1];
-#pragma unroll
-            for (int k = kGlrDx; k <= kGlrDz; ++k)
-                to[k - kGlrDx] = p.rows[k].p + e.off[k] + (int64_t)p.rows[k].ts * (warp * TOK + TOK - 1) +
-                                 2 * lane * (int)sizeof(T);
-            auto put = [&](int tensor, int j, float2 v) {
-                glr_st2<VEC>(reinterpret_cast<T*>(to[tensor - kGlrDx] - (TOK - 1 - j) * (int64_t)p.rows[tensor].ts), v, nch);
-            };
-            auto outputs = [&](auto full) {
-#pragma unroll
-                for (int j = TOK - 1; j >= 0; --j) {
-                    if (!decltype(full)::value && j >= n) continue;
-                    const float2 a = glr_one_minus(u[j]), b2 = glr_mul(u[j], glr_add(a, 1.f));
-                    const float2 b2t = glr_add(b2, kGlrTiny);
-                    const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
-                    const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
-                    float2 dh = glr_row(in_d, j);
-                    if constexpr (EPI == 2) {
-                        const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
-                        const float2 h = glr_add(glr_fma(a, hp[j], w), glr_row(in_add, j));
-                        // silu'(z) = s (1 + z (1 - s))
-                        const float2 ds = glr_mul(sz, glr_fma(z, glr_one_minus(sz), 1.f));
-                        put(kGlrDz, j, glr_mul(glr_mul(dh, h), ds));
-                        dh = glr_mul(dh, glr_mul(z, sz));
-                    }
-                    if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);
-                    const float2 G = glr_add(dh, q);
-                    q = glr_mul(a, G);
-                    const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
-                    const float2 dla = glr_mul(G, glr_sub(glr_mul(a, hp[j]), glr_mul(glr_mul(ab, ab), w)));
-                    const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_one_minus(rg[j])));
-                    const float2 di = glr_mul(glr_mul(G, w), glr_one_minus(ig[j]));
-                    put(kGlrDx, j, glr_mul(G, bi));
-                    put(kGlrDr, j, dr);
-                    put(kGlrDi, j, di);
-                    sA = glr_fma(rg[j], dla, sA);
-                    sr = glr_add(sr, dr);
-                    si = glr_add(si, di);
-                }
-            };
-            if (n == TOK)
-                outputs(std::true_type{});
-            else
-                outputs(std::false_type{});
-        } else {
-            __syncthreads();  // the sums of the tile before are read
+        for (int w = kGlrWarps - 1; w > 0; --w) {
+            const float4 a = agg[w][lane];
+            if (w <= warp) continue;
+            Pw = glr_mul(Pw, make_float2(a.x, a.z));
+            qw = glr_apply(a, qw);
         }
+        q = glr_fma(P, qw, q);
+        P = glr_mul(P, Pw);
+        if (publish && warp == 0) glr_publish_map(glr_map(y, t, t.at), P, q);
+        float4 mypiece = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t.at) {
+            mypiece = glr_wait_piece(y, piece, t, warp);
+        } else if (warp == kGlrGroup - 1) {
+            const float2 c = glr_vec2<VEC>(p.dh_out, row, nch);
+            mypiece = make_float4(0.f, c.x, 0.f, c.y);
+        }
+        pieces[warp][lane] = mypiece;
+        // the states before the warp's steps, from the one that enters the tile
+        if (n) {
+            float2 c = entering;
+#pragma unroll
+            for (int w = 0; w < kGlrWarps - 1; ++w) {
+                const float4 a = agg[w][lane];
+                const float2 hw = aggh[w][lane];
+                if (w < warp) c = glr_fma(make_float2(a.x, a.z), c, hw);
+            }
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                hp[j] = glr_add(c, hp[j]);
+                c = glr_sub(c, glr_mul(u[j], c));
+            }
+        }
+        __syncthreads();
+        const float4 from = pieces[kGlrGroup - 1][lane];
+        float2 c = make_float2(from.y, from.w);
+        c = glr_through(pieces, c, t.at % kGlrGroup);
+        if (warp == 0) {
+            const float2 end = glr_fma(P, c, q);
+            // the other tiles take the last state's gradient from here, not from dh_out, which may be dh_in
+            if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
+            if (publish && (t.at + 1) % kGlrGroup == 0)
+                glr_publish_state(glr_state(y, t, t.at + 1), end);
+            if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
+        }
+        q = glr_fma(Pw, c, qw);
+        const float2 A = glr_vec2<VEC>(p.A, c0, nch);
+        // where the warp's steps go, from its last to its first
+        char* to[kGlrDz - kGlrDx + 1];
+#pragma unroll
+        for (int k = kGlrDx; k <= kGlrDz; ++k)
+            to[k - kGlrDx] = p.rows[k].p + e.off[k] + (int64_t)p.rows[k].ts * (warp * TOK + TOK - 1) +
+                             2 * lane * (int)sizeof(T);
+        auto put = [&](int tensor, int j, float2 v) {
+            glr_st2<VEC>(reinterpret_cast<T*>(to[tensor - kGlrDx] - (TOK - 1 - j) * (int64_t)p.rows[tensor].ts), v, nch);
+        };
+        auto outputs = [&](auto full) {
+#pragma unroll
+            for (int j = TOK - 1; j >= 0; --j) {
+                if (!decltype(full)::value && j >= n) continue;
+                const float2 a = glr_one_minus(u[j]), b2 = glr_mul(u[j], glr_add(a, 1.f));
+                const float2 b2t = glr_add(b2, kGlrTiny);
+                const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
+                const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
+                float2 dh = glr_row(in_d, j);
+                if constexpr (EPI == 2) {
+                    const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
+                    const float2 h = glr_add(glr_fma(a, hp[j], w), glr_row(in_add, j));
+                    // silu'(z) = s (1 + z (1 - s))
+                    const float2 ds = glr_mul(sz, glr_fma(z, glr_one_minus(sz), 1.f));
+                    put(kGlrDz, j, glr_mul(glr_mul(dh, h), ds));
+                    dh = glr_mul(dh, glr_mul(z, sz));
+                }
+                if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);
+                const float2 G = glr_add(dh, q);
+                q = glr_mul(a, G);
+                const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
+                const float2 dla = glr_mul(G, glr_sub(glr_mul(a, hp[j]), glr_mul(glr_mul(ab, ab), w)));
+                const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_one_minus(rg[j])));
+                const float2 di = glr_mul(glr_mul(G, w), glr_one_minus(ig[j]));
+                put(kGlrDx, j, glr_mul(G, bi));
+                put(kGlrDr, j, dr);
+                put(kGlrDi, j, di);
+                sA = glr_fma(rg[j], dla, sA);
+                sr = glr_add(sr, dr);
+                si = glr_add(si, di);
+            }
+        };
+        if (n == TOK)
+            outputs(std::true_type{});
+        else
+            outputs(std::false_type{});
         sums[0][warp][lane] = sA;
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
@@ -889,6 +951,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
     __syncthreads();
     put_sums();
     cp_async_wait_all();
+    if (p.lengths) glr_pad<T>(p, y, reinterpret_cast<unsigned*>(queue));
 }
 
 // The three sums over the partial rows [n][3][D]: a block takes 32 columns, each

@@ -117,21 +117,39 @@ size_t sync_bytes(int batch, int D, int64_t tiles) {
     return 256 + chains * bimamba::kGlrSlab * ((size_t)tiles * 8 + groups * 4);
 }
 
+// With the plan of a padded batch behind it.
+size_t handover_bytes(int batch, int D, int64_t tiles) {
+    return sync_bytes(batch, D, tiles) + 16 * ((size_t)batch * tiles + 1);
+}
+
 // Points y at the workspace and enqueues the all-ones fill (a row of one tile
-// hands nothing over and gets neither).
-int make_sync(bimamba::GlrSync& y, int batch, int D, int64_t tiles, unsigned flags, void* ws, cudaStream_t st) {
+// hands nothing over and gets neither), and what a padded batch needs first.
+int make_sync(bimamba::GlrSync& y, const GlrParams& k, int64_t tiles, int tile_steps, unsigned flags, void* ws,
+              cudaStream_t st) {
+    const int batch = k.batch, D = k.D;
+    const size_t bytes = tiles > 1 ? sync_bytes(batch, D, tiles) : 0;
+    int4* plan = k.lengths && tiles > 1 ? reinterpret_cast<int4*>(static_cast<char*>(ws) + bytes) : nullptr;
+    if (plan) {
+        const int64_t blocks = std::max<int64_t>(k.batch * tiles, (int64_t)(bytes / 16384));
+        bimamba::glr_plan_kernel<<<(unsigned)std::min<int64_t>(blocks, 8 * kSms), 256, 0, st>>>(
+            k, static_cast<uint4*>(ws), (int64_t)bytes, plan, tiles, tile_steps);
+        const int rc = launch_status();
+        if (rc) return rc;
+    }
     y = {};
     y.tiles = tiles;
     y.groups = (tiles + bimamba::kGlrGroup - 1) / bimamba::kGlrGroup;
     if (tiles <= 1) return BIMAMBA_OK;
     const size_t chains = (size_t)batch * ((D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    y.plan = plan;
     y.starve = (flags & BIMAMBA_TEST_STARVE) ? 1 : 0;
     y.wait_limit = y.starve ? kStarveWaitCycles : kWaitCycles;
     unsigned char* q = static_cast<unsigned char*>(ws);
     y.ticket = reinterpret_cast<unsigned int*>(q);
     y.map = reinterpret_cast<unsigned long long*>(q + 256);
     y.state = reinterpret_cast<float*>(q + 256 + chains * bimamba::kGlrSlab * (size_t)tiles * 8);
-    return cudaMemsetAsync(ws, 0xff, sync_bytes(batch, D, tiles), st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
+    if (plan) return BIMAMBA_OK;
+    return cudaMemsetAsync(ws, 0xff, bytes, st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
 }
 
 // Every row of the tensors from first to last starts at a multiple of `bytes`.
@@ -158,13 +176,13 @@ bool pairs(const GlrParams& k, int esz) {
 }
 
 // Blocks that stay: what the SMs hold at 128 registers a thread.
-int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, int64_t tiles, int warps,
+int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, int64_t tiles, int tile_steps, int warps,
                  size_t warp_bytes, unsigned flags, void* ws, cudaStream_t st) {
     const int64_t total = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
     // tickets run past the total by what the blocks take ahead
     if (total > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
     bimamba::GlrSync y;
-    int rc = make_sync(y, k.batch, k.D, tiles, flags, ws, st);
+    int rc = make_sync(y, k, tiles, tile_steps, flags, ws, st);
     if (rc) return rc;
     y.total = (unsigned)total;
     const size_t smem = warps * warp_bytes;
@@ -181,13 +199,13 @@ int launch_fwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st
     constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
     const int64_t tiles = (k.L + TILE - 1) / TILE;
     const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
-    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI>, k, tiles, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
+    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI>, k, tiles, TILE, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
                         flags, ws, st);
 }
 
 template <typename T, bool VEC, int EPI>
 int launch_bwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
-    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI>, k, k.nchunk, bimamba::kGlrWarps,
+    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI>, k, k.nchunk, bimamba::kGlrChunk, bimamba::kGlrWarps,
                         bimamba::kGlrBwdWarpBytes<T, EPI>, flags, ws, st);
 }
 
@@ -225,7 +243,7 @@ extern "C" {
 
 size_t bimamba_glr_workspace_bytes(int batch, int64_t L, int d_inner, int backward) {
     if (!sizes_ok(batch, L, d_inner)) return 0;
-    const size_t sync = sync_bytes(batch, d_inner, (L + kSmallTile - 1) / kSmallTile);
+    const size_t sync = handover_bytes(batch, d_inner, (L + kSmallTile - 1) / kSmallTile);
     return backward ? part_bytes(batch, L, d_inner) + sync : sync;
 }
 
