@@ -113,11 +113,15 @@ struct GlrRaw<__nv_bfloat16> {
     __device__ __forceinline__ float2 get() const {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
+    __device__ __forceinline__ float2 neg() const {
+        return make_float2(__uint_as_float((v << 16) + 0x80000000u), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u));
+    }
 };
 template <>
 struct GlrRaw<float> {
     float2 v;
     __device__ __forceinline__ float2 get() const { return v; }
+    __device__ __forceinline__ float2 neg() const { return make_float2(-v.x, -v.y); }
 };
 
 // Stores of n (0..2) channels of a pair.  VEC: one access (channel count and
@@ -151,13 +155,13 @@ __device__ __forceinline__ float2 glr_vec2(const float* p, int64_t c, int n) {
 
 __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(glr_sigmoid(v.x), glr_sigmoid(v.y)); }
 
-// u = 1 - 2^l for l <= 0, to fp32's relative accuracy however small |l| is, on
-// the FP32 pipe (the special-function unit is the forward's scarcest): l =
-// n + f with |f| <= 1/2 (n by adding and subtracting 1.5 2^23), 2^f - 1 = f p(f)
-// with p of degree 5 (minimax of the relative error by Remez exchange, 1.1e-8),
-// and u = (1 - 2^n) - 2^n (2^f - 1), where 1 - 2^n is exact or far from
+// 2^l - 1 for l <= 0, to fp32's relative accuracy however small |l| is, on the
+// FP32 pipe (the special-function unit is the forward's scarcest): l = n + f
+// with |f| <= 1/2 (n by adding and subtracting 1.5 2^23), 2^f - 1 = f p(f) with
+// p of degree 5 (minimax of the relative error by Remez exchange, 1.1e-8), and
+// 2^l - 1 = (2^n - 1) + 2^n (2^f - 1), where 2^n - 1 is exact or far from
 // cancelling.  Below l = -126 the power is as good as 0.
-__device__ __forceinline__ float2 glr_one_minus_ex2(float2 l) {
+__device__ __forceinline__ float2 glr_ex2m1(float2 l) {
     constexpr float kMagic = 12582912.f;
     l = make_float2(glr_max_nan(l.x, -126.f), glr_max_nan(l.y, -126.f));
     const float2 m = glr_add(l, kMagic);
@@ -168,39 +172,37 @@ __device__ __forceinline__ float2 glr_one_minus_ex2(float2 l) {
     q = glr_fma(f, q, 0.24022649228572845f);
     q = glr_fma(f, q, 0.6931471824645996f);
     q = glr_mul(f, q);
-    // -2^n, its exponent from the low bits of m
-    const float2 s = make_float2(__uint_as_float((__float_as_uint(m.x) << 23) + 0xbf800000u),
-                                 __uint_as_float((__float_as_uint(m.y) << 23) + 0xbf800000u));
-    return glr_fma(q, s, glr_add(s, 1.f));
+    // 2^n, its exponent from the low bits of m
+    const float2 s = make_float2(__uint_as_float((__float_as_uint(m.x) << 23) + 0x3f800000u),
+                                 __uint_as_float((__float_as_uint(m.y) << 23) + 0x3f800000u));
+    return glr_fma(q, s, glr_add(s, -1.f));
 }
 
-__device__ __forceinline__ float2 glr_one_minus(float2 v) {
-    return glr_fma(v, glr_f2(-1.f), glr_f2(1.f));
-}
-
-// The gates of a pair: r, i raw activations; nr, ni: -bias log2 e; A2: A log2 e.
+// The gates of a pair, most of them negated: so the products and sums below
+// need no operand of ones, which costs two registers or two moves each time.
+// r, i: raw activations; nr, ni: -bias log2 e; nA2: -A log2 e.
 struct GlrGate2 {
-    float2 rg, u, a, b2, di;  // a = 1 - u, b2 = beta^2 = 1 - a^2 = u (1 + a), ig = 1 / di
+    float2 nrg, nu, a, nb2, di;  // -rg, a - 1, a, -beta^2 = a^2 - 1, 1 / ig
 };
-__device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 A2) {
+__device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 nA2) {
     GlrGate2 g;
     const float2 er = glr_fma(r, glr_f2(-kGlrLog2e), nr), ei = glr_fma(i, glr_f2(-kGlrLog2e), ni);
     const float2 dr = glr_add(make_float2(glr_ex2(er.x), glr_ex2(er.y)), 1.f);
     g.di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), 1.f);
-    g.rg = make_float2(glr_rcp(dr.x), glr_rcp(dr.y));
-    g.u = glr_one_minus_ex2(glr_mul(A2, g.rg));
-    g.a = glr_one_minus(g.u);
-    g.b2 = glr_mul(g.u, glr_add(g.a, 1.f));
+    g.nrg = make_float2(glr_rcp(-dr.x), glr_rcp(-dr.y));
+    g.nu = glr_ex2m1(glr_mul(nA2, g.nrg));
+    g.a = glr_add(g.nu, 1.f);
+    g.nb2 = glr_fma(g.nu, g.a, g.nu);
     return g;
 }
 // The smallest normal, added under every 1 / beta: 0 / 0 becomes 0, and down to
 // beta^2 = 1e-31 nothing else changes.
 constexpr float kGlrTiny = 1.17549435e-38f;
-// beta ig with one special function: b2 / sqrt(b2 di^2) = sqrt(b2) / di (where
+// -beta ig with one special function: b2 / sqrt(b2 di^2) = sqrt(b2) / di (where
 // di^2 overflows, an input gate below e^-44, it counts as closed).
-__device__ __forceinline__ float2 glr_beta_ig(float2 b2, float2 di) {
-    const float2 v = glr_mul(glr_mul(glr_add(b2, kGlrTiny), di), di);
-    return glr_mul(b2, make_float2(glr_rsqrt(v.x), glr_rsqrt(v.y)));
+__device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
+    const float2 v = glr_mul(glr_mul(make_float2(kGlrTiny - nb2.x, kGlrTiny - nb2.y), di), di);
+    return glr_mul(nb2, make_float2(glr_rsqrt(v.x), glr_rsqrt(v.y)));
 }
 
 // ---------------------------------------------------------------- tiles in scan order
@@ -572,7 +574,11 @@ template <bool VEC>
 __device__ __forceinline__ float2 glr_scaled(const float* v, int c, int nch, float by) {
     return glr_finite(glr_mul(glr_vec2<VEC>(v, c, nch), glr_f2(by)));
 }
-// The lane's pair of row j.
+// The lane's pair of row j, and its negative.
+template <typename T>
+__device__ __forceinline__ float2 glr_minus_row(const T* rows, int j) {
+    return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].neg();
+}
 template <typename T>
 __device__ __forceinline__ float2 glr_row(const T* rows, int j) {
     return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].get();
@@ -647,14 +653,14 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if (n) {
             T* in = mine + stage * 3 * ROWS;
             if (n < TOK) glr_close_rows<T, TOK>(in, n);
-            const float2 A2 = glr_scaled<VEC>(p.A, c0, nch, kGlrLog2e);
+            const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
             float2 P = glr_f2(1.f), h = glr_f2(0.f);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
-                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
-                const float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in + 2 * ROWS, j));
+                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, nA2);
+                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in + 2 * ROWS, j));
                 P = glr_mul(P, g.a);
                 h = glr_fma(g.a, h, w);
                 Ps[j] = P;
@@ -807,23 +813,23 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if (t.at) glr_ask(piece, y, t, warp);
         T* in = mine + stage * NT * ROWS;
         const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_z = in + 4 * ROWS, *in_add = in + 5 * ROWS;
-        float2 rg[TOK], ig[TOK], u[TOK], hp[TOK];
+        float2 nrg[TOK], nig[TOK], nu[TOK], hp[TOK];
         const float2 entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
         cp_async_wait_pending<NS - 1>();
         __syncwarp();
         float2 P = glr_f2(1.f), q = glr_f2(0.f), h = glr_f2(0.f);
         if (n) {
             if (n < TOK) glr_close_rows<T, TOK>(in, n);
-            const float2 A2 = glr_scaled<VEC>(p.A, c0, nch, kGlrLog2e);
+            const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
-                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, A2);
-                const float2 w = glr_mul(glr_beta_ig(g.b2, g.di), glr_row(in_x, j));
-                rg[j] = g.rg;
-                ig[j] = make_float2(glr_rcp(g.di.x), glr_rcp(g.di.y));
-                u[j] = g.u;
+                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, nA2);
+                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in_x, j));
+                nrg[j] = g.nrg;
+                nig[j] = make_float2(glr_rcp(-g.di.x), glr_rcp(-g.di.y));
+                nu[j] = g.nu;
                 hp[j] = h;  // the state before step j, from a zero state at the warp's first
                 P = glr_mul(P, g.a);
                 h = glr_fma(g.a, h, w);
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                     dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
                 }
                 const float2 G = glr_add(q, dh);
-                q = glr_sub(G, glr_mul(u[j], G));  // a G
+                q = glr_fma(nu[j], G, G);  // a G
             }
         }
         aggh[warp][lane] = h;
@@ -880,7 +886,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 hp[j] = glr_add(c, hp[j]);
-                c = glr_sub(c, glr_mul(u[j], c));
+                c = glr_fma(nu[j], c, c);
             }
         }
         __syncthreads();
@@ -896,7 +902,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
         }
         q = glr_fma(Pw, c, qw);
-        const float2 A = glr_vec2<VEC>(p.A, c0, nch);
+        const float2 nA = glr_mul(glr_vec2<VEC>(p.A, c0, nch), glr_f2(-1.f));
         // where the warp's steps go, from its last to its first
         char* to[kGlrDz - kGlrDx + 1];
 #pragma unroll
@@ -910,30 +916,32 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = TOK - 1; j >= 0; --j) {
                 if (!decltype(full)::value && j >= n) continue;
-                const float2 a = glr_one_minus(u[j]), b2 = glr_mul(u[j], glr_add(a, 1.f));
-                const float2 b2t = glr_add(b2, kGlrTiny);
-                const float2 rb = make_float2(glr_rsqrt(b2t.x), glr_rsqrt(b2t.y));  // 1 / beta
-                const float2 bi = glr_mul(glr_mul(b2, rb), ig[j]), w = glr_mul(bi, glr_row(in_x, j));
+                const float2 nb2 = glr_fma(nu[j], nu[j], glr_add(nu[j], nu[j]));
+                // 1 / beta
+                const float2 rb = make_float2(glr_rsqrt(kGlrTiny - nb2.x), glr_rsqrt(kGlrTiny - nb2.y));
+                const float2 bi = glr_mul(glr_mul(nb2, rb), nig[j]);  // beta ig
+                const float2 w = glr_mul(bi, glr_row(in_x, j));
+                const float2 h = glr_add(glr_fma(nu[j], hp[j], hp[j]), w);
                 float2 dh = glr_row(in_d, j);
                 if constexpr (EPI == 2) {
                     const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
-                    const float2 h = glr_add(glr_fma(a, hp[j], w), glr_row(in_add, j));
                     // silu'(z) = s (1 + z (1 - s))
-                    const float2 ds = glr_mul(sz, glr_fma(z, glr_one_minus(sz), 1.f));
-                    put(kGlrDz, j, glr_mul(glr_mul(dh, h), ds));
+                    const float2 ds = glr_fma(glr_mul(sz, z), make_float2(1.f - sz.x, 1.f - sz.y), sz);
+                    put(kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add, j))), ds));
                     dh = glr_mul(dh, glr_mul(z, sz));
                 }
                 if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);
                 const float2 G = glr_add(dh, q);
-                q = glr_mul(a, G);
-                const float2 ab = glr_mul(a, rb);  // (a^2 / beta^2) w below
-                const float2 dla = glr_mul(G, glr_sub(glr_mul(a, hp[j]), glr_mul(glr_mul(ab, ab), w)));
-                const float2 dr = glr_mul(glr_mul(A, dla), glr_mul(rg[j], glr_one_minus(rg[j])));
-                const float2 di = glr_mul(glr_mul(G, w), glr_one_minus(ig[j]));
+                q = glr_fma(nu[j], G, G);
+                // a h_{s-1} - (a^2 / beta^2) w = h - w / beta^2 (both 0 with beta)
+                const float2 wb = glr_mul(w, rb);
+                const float2 dla = glr_mul(G, make_float2(fmaf(-wb.x, rb.x, h.x), fmaf(-wb.y, rb.y, h.y)));
+                const float2 dr = glr_mul(glr_mul(nA, dla), glr_fma(nrg[j], nrg[j], nrg[j]));
+                const float2 Gw = glr_mul(G, w), di = glr_fma(Gw, nig[j], Gw);
                 put(kGlrDx, j, glr_mul(G, bi));
                 put(kGlrDr, j, dr);
                 put(kGlrDi, j, di);
-                sA = glr_fma(rg[j], dla, sA);
+                sA = glr_fma(nrg[j], dla, sA);
                 sr = glr_add(sr, dr);
                 si = glr_add(si, di);
             }
@@ -942,7 +950,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             outputs(std::true_type{});
         else
             outputs(std::false_type{});
-        sums[0][warp][lane] = sA;
+        sums[0][warp][lane] = make_float2(-sA.x, -sA.y);
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
         __syncwarp();  // every lane has read its rows
