@@ -508,51 +508,63 @@ __device__ __forceinline__ int glr_steps(int64_t len, int64_t ws, int most) {
     return len - ws >= most ? most : (len > ws ? (int)(len - ws) : 0);
 }
 
-// A warp's copy of n rows (of TOK) of one tensor into its place: row j is the
-// tile's step first + j, `left` channels wide.  The widest copies that the
-// launch found possible; what lies past n or past the last channel becomes 0.
-template <typename T, int TOK>
-__device__ __forceinline__ void glr_copy_rows(T* to, const GlrParams& p, const GlrEntry& e, int tensor, int first, int n,
-                                              int left) {
+// A warp's copy of n rows (of TOK) of some tensors into their places, one
+// behind the other: row j is the tile's step first + j, `left` channels wide.
+// The widest copies that the launch found possible; what lies past n or past
+// the last channel becomes 0.
+template <typename T, int TOK, int... TENSORS>
+__device__ __forceinline__ void glr_copy_rows(T* to, const GlrParams& p, const GlrEntry& e, int first, int n, int left) {
     const int lane = threadIdx.x & 31;
-    const char* const tile = p.rows[tensor].p + e.off[tensor];
-    const int64_t ts = p.rows[tensor].ts;
-    if (p.copy == 16) {
-        constexpr int E = 16 / sizeof(T), PER = kGlrSlab / E, ROWS = 32 / PER;  // elements a copy, copies a row
-        const int col = lane % PER * E, r = lane / PER;
-        const char* from = tile + (first + r) * ts + col * sizeof(T);
-        to += r * kGlrSlab + col;
-        if (n == TOK && left >= kGlrSlab) {
-#pragma unroll
-            for (int k = 0; k < TOK / ROWS; ++k) cp_async<16>(to + k * ROWS * kGlrSlab, from + k * ROWS * ts, true);
-        } else {
+    constexpr int E = 16 / sizeof(T), PER = kGlrSlab / E, ROWS = 32 / PER;  // elements a copy, copies a row
+    if (p.copy == 16 && n == TOK && left >= kGlrSlab) {
+        const int r = first + lane / PER, col = lane % PER * 16;
+        uint32_t dst = smem_addr(to) + lane * 16;
+        const auto one = [&](int tensor) {
+            const int64_t ts = p.rows[tensor].ts;
+            const char* from = p.rows[tensor].p + (e.off[tensor] + col) + r * ts;
 #pragma unroll
             for (int k = 0; k < TOK / ROWS; ++k) {
-                const bool ok = col < left && r + k * ROWS < n;
-                cp_async<16>(to + k * ROWS * kGlrSlab, ok ? from + k * ROWS * ts : tile, ok);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 512), "l"(from) : "memory");
+                from += ROWS * ts;
             }
-        }
-    } else if (p.copy) {
-        const int col = 2 * lane;
-        const char* from = tile + first * ts + col * sizeof(T);
-#pragma unroll 4
-        for (int j = 0; j < TOK; ++j) {
-            const bool ok = col < left && j < n;
-            cp_async<2 * sizeof(T)>(to + j * kGlrSlab + col, ok ? from + j * ts : tile, ok);
-        }
-    } else {
-        T v[TOK][2];
-        const int col = 2 * lane;
-        const char* from = tile + first * ts + col * sizeof(T);
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const T* q = reinterpret_cast<const T*>(from + j * ts);
-            v[j][0] = j < n && col < left ? q[0] : T(0.f);
-            v[j][1] = j < n && col + 1 < left ? q[1] : T(0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) to[j * kGlrSlab + col] = v[j][0], to[j * kGlrSlab + col + 1] = v[j][1];
+            dst += TOK * kGlrSlab * sizeof(T);
+        };
+        (one(TENSORS), ...);
+        return;
     }
+    const auto one = [&](int tensor) {
+        const char* const tile = p.rows[tensor].p + e.off[tensor];
+        const int64_t ts = p.rows[tensor].ts;
+        const int col = 2 * lane;
+        if (p.copy == 16) {
+            const int col = lane % PER * E, r = lane / PER;
+            const char* from = tile + (first + r) * ts + col * sizeof(T);
+            for (int k = 0; k < TOK / ROWS; ++k) {
+                const bool ok = col < left && r + k * ROWS < n;
+                cp_async<16>(to + (r + k * ROWS) * kGlrSlab + col, ok ? from + k * ROWS * ts : tile, ok);
+            }
+        } else if (p.copy) {
+            const char* from = tile + first * ts + col * sizeof(T);
+#pragma unroll 4
+            for (int j = 0; j < TOK; ++j) {
+                const bool ok = col < left && j < n;
+                cp_async<2 * sizeof(T)>(to + j * kGlrSlab + col, ok ? from + j * ts : tile, ok);
+            }
+        } else {
+            T v[TOK][2];
+            const char* from = tile + first * ts + col * sizeof(T);
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                const T* q = reinterpret_cast<const T*>(from + j * ts);
+                v[j][0] = j < n && col < left ? q[0] : T(0.f);
+                v[j][1] = j < n && col + 1 < left ? q[1] : T(0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) to[j * kGlrSlab + col] = v[j][0], to[j * kGlrSlab + col + 1] = v[j][1];
+        }
+        to += TOK * kGlrSlab;
+    };
+    (one(TENSORS), ...);
 }
 // Steps past a warp's last keep the state: their rows (zeros so far) get a
 // closed gate r = -inf, so that a = 1 and w = 0 without a select in the scan.
@@ -609,10 +621,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const int n = t.at < 0 ? 0 : glr_steps(t.len, (int64_t)t.at * tile_steps + warp * TOK, TOK);
         if (n) {
             const int left = p.D - glr_channel(p, t);
-            T* to = mine + stage * 3 * ROWS;
-            glr_copy_rows<T, TOK>(to, p, e, kGlrR, warp * TOK, n, left);
-            glr_copy_rows<T, TOK>(to + ROWS, p, e, kGlrI, warp * TOK, n, left);
-            glr_copy_rows<T, TOK>(to + 2 * ROWS, p, e, kGlrX, warp * TOK, n, left);
+            glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, p, e, warp * TOK, n, left);
         }
         cp_async_commit();
     };
@@ -645,9 +654,9 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if constexpr (EPI > 0) {
             // every lane is past its last tile's outputs
             const int left = p.D - (c0 - 2 * lane);
-            if (EPI == 2 && n) glr_copy_rows<T, TOK>(epi, p, e, kGlrZ, warp * TOK, n, left);
+            if (EPI == 2 && n) glr_copy_rows<T, TOK, kGlrZ>(epi, p, e, warp * TOK, n, left);
             if (n && p.rows[kGlrAdd].p)
-                glr_copy_rows<T, TOK>(epi + (EPI - 1) * ROWS, p, e, kGlrAdd, warp * TOK, n, left);
+                glr_copy_rows<T, TOK, kGlrAdd>(epi + (EPI - 1) * ROWS, p, e, warp * TOK, n, left);
             cp_async_commit();
         }
         if (n) {
@@ -767,13 +776,11 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if (n) {
             const int left = p.D - glr_channel(p, t);
             T* to = mine + stage * NT * ROWS;
-            glr_copy_rows<T, TOK>(to, p, e, kGlrR, warp * TOK, n, left);
-            glr_copy_rows<T, TOK>(to + ROWS, p, e, kGlrI, warp * TOK, n, left);
-            glr_copy_rows<T, TOK>(to + 2 * ROWS, p, e, kGlrX, warp * TOK, n, left);
-            glr_copy_rows<T, TOK>(to + 3 * ROWS, p, e, kGlrDout, warp * TOK, n, left);
             if constexpr (EPI == 2) {
-                glr_copy_rows<T, TOK>(to + 4 * ROWS, p, e, kGlrZ, warp * TOK, n, left);
-                if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK>(to + 5 * ROWS, p, e, kGlrAdd, warp * TOK, n, left);
+                glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ>(to, p, e, warp * TOK, n, left);
+                if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK, kGlrAdd>(to + 5 * ROWS, p, e, warp * TOK, n, left);
+            } else {
+                glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout>(to, p, e, warp * TOK, n, left);
             }
         }
         cp_async_commit();
