@@ -816,6 +816,355 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(c
     }
 }
 
+// ---------------------------------------------------------------- rows of any width, packed
+
+// Rows that are no whole groups of eight, or too narrow for a warp.  A block
+// takes a tile of neighbouring rows as the flat run of bytes that it is:
+// 16-byte chunks copied ahead into one of two stages and, with the results
+// in the places of the inputs, written back the same way, whatever the width.  A
+// group of G lanes (4 to 32, or the whole block) has a row, E elements a lane,
+// P of them (2 for even widths) in one access: lane g's j-th access is
+// column (g + G j) P.
+
+// A tile's bytes of one tensor: [at, at + bytes) from the 16-byte aligned base;
+// in shared memory the chunk that holds `at` comes first.
+struct BnRun {
+    int64_t at;
+    int bytes;
+    __device__ __forceinline__ int head() const { return (int)(at & 15); }
+    __device__ __forceinline__ int chunks() const { return (head() + bytes + 15) >> 4; }
+};
+// `end`: the tensor's bytes, past which nothing is read.
+__device__ __forceinline__ void bn_copy_run(unsigned char* to, const void* base, BnRun r, int64_t end) {
+    const char* from = static_cast<const char*>(base) + (r.at & ~15LL);
+    const int64_t left = end - (r.at & ~15LL);
+    for (int k = threadIdx.x; k < r.chunks(); k += blockDim.x) {
+        const int n = left - 16LL * k < 16 ? (int)(left - 16LL * k) : 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to) + 16 * k), "l"(from + 16LL * k),
+                     "r"(n)
+                     : "memory");
+    }
+}
+template <typename T>
+__device__ __forceinline__ void bn_store_run(const unsigned char* from, void* base, BnRun r) {
+    char* to = static_cast<char*>(base) + (r.at & ~15LL);
+    const int head = r.head(), tail = head + r.bytes;  // the chunks' bytes [head, tail) are the run's
+    for (int k = threadIdx.x; k < r.chunks(); k += blockDim.x) {
+        if (16 * k >= head && 16 * k + 16 <= tail) {
+            *reinterpret_cast<uint4*>(to + 16LL * k) = *reinterpret_cast<const uint4*>(from + 16 * k);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += (int)sizeof(T))
+                if (16 * k + e >= head && 16 * k + e < tail)
+                    *reinterpret_cast<T*>(to + 16LL * k + e) = *reinterpret_cast<const T*>(from + 16 * k + e);
+        }
+    }
+}
+
+template <int P>
+__device__ __forceinline__ void bn_get(const __nv_bfloat16* p, float* v) {
+    if constexpr (P == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+template <int P>
+__device__ __forceinline__ void bn_get(const float* p, float* v) {
+    if constexpr (P == 2) {
+        const float2 w = *reinterpret_cast<const float2*>(p);
+        v[0] = w.x, v[1] = w.y;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int P>
+__device__ __forceinline__ void bn_set(__nv_bfloat16* p, const float* v) {
+    if constexpr (P == 2)
+        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
+    else
+        *p = __float2bfloat16_rn(v[0]);
+}
+template <int P>
+__device__ __forceinline__ void bn_set(float* p, const float* v) {
+    if constexpr (P == 2)
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else
+        *p = v[0];
+}
+
+// A lane's E elements of a row, or of an fp32 vector (`other` without it, 0 past d).
+template <int E, int P, typename T>
+__device__ __forceinline__ void bn_gather(const T* row, float (&v)[E], int g, int G, int d) {
+#pragma unroll
+    for (int j = 0; j < E / P; ++j) {
+        const int c = (g + G * j) * P;
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[j * P + e] = 0.f;
+        if (c < d) bn_get<P>(row + c, v + j * P);
+    }
+}
+template <int E, int P, typename T>
+__device__ __forceinline__ void bn_scatter(T* row, const float (&v)[E], int g, int G, int d) {
+#pragma unroll
+    for (int j = 0; j < E / P; ++j) {
+        const int c = (g + G * j) * P;
+        if (c < d) bn_set<P>(row + c, v + j * P);
+    }
+}
+template <int E, int P>
+__device__ __forceinline__ void bn_gather_vec(const float* p, float other, float (&v)[E], int g, int G, int d) {
+#pragma unroll
+    for (int j = 0; j < E / P; ++j)
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            const int c = (g + G * j) * P + e;
+            v[j * P + e] = c < d ? (p ? p[c] : other) : 0.f;
+        }
+}
+// The row's sums of a pair: G lanes, or (G = the block) through shared memory.
+__device__ __forceinline__ float2 bn_group_sum2(float2 v, int G, BnShared& sh, int& turn) {
+    if (G > 32) return bn_block_sum2(v, sh, turn);
+    for (int off = G >> 1; off > 0; off >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    }
+    return v;
+}
+template <int E, int P>
+__device__ __forceinline__ float2 bn_group_stats(const float (&v)[E], const BlockNormParams& p, int g, int G,
+                                                 BnShared& sh, int& turn) {
+    const float per = 1.f / (float)p.d;
+    float mu = 0.f, q = 0.f;
+    if (!p.rms) {
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) t += v[e];  // columns past d hold 0
+        mu = bn_group_sum2(make_float2(t, 0.f), G, sh, turn).x * per;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float c = v[e] - mu;
+        if ((g + G * (e / P)) * P < p.d) q = fmaf(c, c, q);
+    }
+    return make_float2(mu, rsqrtf(bn_group_sum2(make_float2(q, 0.f), G, sh, turn).x * per + p.eps));
+}
+
+constexpr int kBnPackFwd = 16, kBnPackBwd = 8;  // E
+// Bytes of a stage: `rows` rows of each tensor (chunks at both ends may be partial).
+__host__ __device__ __forceinline__ int bn_pack_bytes(int rows, int d, int esz) { return (rows * d * esz + 31 + 15) / 16 * 16; }
+
+template <typename TS, typename TU, int P, bool POST>
+__global__ void __launch_bounds__(256, 2) block_norm_fwd_pack_kernel(const BlockNormParams p, const int G, const int R) {
+    constexpr int E = kBnPackFwd;
+    extern __shared__ __align__(16) unsigned char bn_smem[];
+    __shared__ BnShared sh;
+    int turn = 0;
+    const int d = p.d, g = threadIdx.x % G, group = threadIdx.x / G, groups = blockDim.x / G;
+    const int64_t b = blockIdx.y, tiles = (p.L + R - 1) / R;
+    const int xs = bn_pack_bytes(R, d, sizeof(TS)), us = bn_pack_bytes(R, d, sizeof(TU));
+    const int64_t all = p.batch * p.L * d;
+    const auto run = [&](int64_t tile, int esz) {
+        const int64_t t0 = tile * R, n = p.L - t0 < R ? p.L - t0 : R;
+        return BnRun{(b * p.L + t0) * d * esz, (int)n * d * esz};
+    };
+    const auto fetch = [&](int64_t tile, int s) {
+        if (tile < tiles) {
+            bn_copy_run(bn_smem + s * (xs + us), p.x, run(tile, sizeof(TS)), all * (int)sizeof(TS));
+            if (p.u) bn_copy_run(bn_smem + s * (xs + us) + xs, p.u, run(tile, sizeof(TU)), all * (int)sizeof(TU));
+        }
+        cp_async_commit();
+    };
+    fetch(blockIdx.x, 0);
+    float gate[E], gamma[E], beta[E], post_w[POST ? E : 1];
+    bn_gather_vec<E, P>(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, gate, g, G, d);
+    if constexpr (POST) bn_gather_vec<E, P>(p.post_w, 1.f, post_w, g, G, d);
+    bn_gather_vec<E, P>(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, gamma, g, G, d);
+    bn_gather_vec<E, P>(p.beta ? p.beta + b * p.gamma_bs : nullptr, 0.f, beta, g, G, d);
+    bn_share(sh, 0.f);
+    int s = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, s ^= 1) {
+        const BnRun rx = run(tile, sizeof(TS)), ru = run(tile, sizeof(TU));
+        const int n = rx.bytes / (d * (int)sizeof(TS));
+        unsigned char* const stage = bn_smem + s * (xs + us);
+        TS* const xt = reinterpret_cast<TS*>(stage + rx.head());
+        TU* const ut = reinterpret_cast<TU*>(stage + xs + ru.head());
+        cp_async_wait_all();
+        __syncthreads();  // and the other stage's results are written back
+        fetch(tile + gridDim.x, s ^ 1);
+        // whole warps (or the block) go round together: a group without a row has one of no columns
+        for (int r0 = 0; r0 < n; r0 += groups) {
+            const bool own = r0 + group < n;
+            const int r = own ? r0 + group : n - 1, w = own ? d : 0;
+            float x[E], u[E];
+            float2 sx = make_float2(0.f, 1.f), su = make_float2(0.f, 1.f);
+            bn_gather<E, P>(xt + r * d, x, g, G, w);
+            if (p.u) {
+                bn_gather<E, P>(ut + r * d, u, g, G, w);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) u[e] = 0.f;
+            }
+            if constexpr (POST) {
+                su = bn_group_stats<E, P>(u, p, g, G, sh, turn);
+#pragma unroll
+                for (int e = 0; e < E; ++e) u[e] = (u[e] - su.x) * su.y * post_w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = bn_round<TS>(fmaf(gate[e], u[e], p.res_scale * x[e]));
+            if (own && p.x_out) bn_scatter<E, P>(xt + r * d, x, g, G, d);
+            if (p.y) {
+                sx = bn_group_stats<E, P>(x, p, g, G, sh, turn);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = fmaf(gamma[e], (x[e] - sx.x) * sx.y, beta[e]);
+                if (own) bn_scatter<E, P>(ut + r * d, x, g, G, d);
+            }
+            if (own && p.stats && g == 0) {
+                float* st = p.stats + (b * p.L + tile * R + r) * 4;
+                st[0] = sx.x, st[1] = sx.y, st[2] = su.x, st[3] = su.y;
+            }
+        }
+        __syncthreads();
+        if (p.x_out) bn_store_run<TS>(stage, p.x_out, rx);
+        if (p.y) bn_store_run<TU>(stage + xs, p.y, ru);
+    }
+    cp_async_wait_all();
+}
+
+template <typename TS, typename TU, int P, bool POST>
+__global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const BlockNormParams p, const int G, const int R) {
+    constexpr int E = kBnPackBwd;
+    extern __shared__ __align__(16) unsigned char bn_smem[];
+    __shared__ BnShared sh;
+    int turn = 0;
+    const int d = p.d, g = threadIdx.x % G, group = threadIdx.x / G, groups = blockDim.x / G;
+    const int64_t b = blockIdx.y, tiles = (p.L + R - 1) / R;
+    const int xs = bn_pack_bytes(R, d, sizeof(TS)), us = bn_pack_bytes(R, d, sizeof(TU));
+    const int64_t all = p.batch * p.L * d;
+    const auto run = [&](int64_t tile, int esz) {
+        const int64_t t0 = tile * R, n = p.L - t0 < R ? p.L - t0 : R;
+        return BnRun{(b * p.L + t0) * d * esz, (int)n * d * esz};
+    };
+    // x_out (then dx), dx_out, u (then du), dy
+    const auto fetch = [&](int64_t tile, int s) {
+        if (tile < tiles) {
+            unsigned char* const stage = bn_smem + s * 2 * (xs + us);
+            const BnRun rx = run(tile, sizeof(TS)), ru = run(tile, sizeof(TU));
+            if (p.dy) bn_copy_run(stage, p.x, rx, all * (int)sizeof(TS));
+            if (p.dx_out) bn_copy_run(stage + xs, p.dx_out, rx, all * (int)sizeof(TS));
+            if (p.u) bn_copy_run(stage + 2 * xs, p.u, ru, all * (int)sizeof(TU));
+            if (p.dy) bn_copy_run(stage + 2 * xs + us, p.dy, ru, all * (int)sizeof(TU));
+        }
+        cp_async_commit();
+    };
+    fetch(blockIdx.x, 0);
+    float gate[E], gamma[E], post_w[POST ? E : 1], sg[E], sw[E], sm[E], sb[E];
+    bn_gather_vec<E, P>(p.gate ? p.gate + b * p.gate_bs : nullptr, 1.f, gate, g, G, d);
+    if constexpr (POST) bn_gather_vec<E, P>(p.post_w, 1.f, post_w, g, G, d);
+    bn_gather_vec<E, P>(p.gamma ? p.gamma + b * p.gamma_bs : nullptr, 1.f, gamma, g, G, d);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sg[e] = sw[e] = sm[e] = sb[e] = 0.f;
+    bn_share(sh, 0.f);
+    const float per = 1.f / (float)d;
+    int s = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, s ^= 1) {
+        const BnRun rx = run(tile, sizeof(TS)), ru = run(tile, sizeof(TU));
+        const int n = rx.bytes / (d * (int)sizeof(TS));
+        unsigned char* const stage = bn_smem + s * 2 * (xs + us);
+        TS* const xt = reinterpret_cast<TS*>(stage + rx.head());
+        const TS* const dxt = reinterpret_cast<const TS*>(stage + xs + rx.head());
+        TU* const ut = reinterpret_cast<TU*>(stage + 2 * xs + ru.head());
+        const TU* const dyt = reinterpret_cast<const TU*>(stage + 2 * xs + us + ru.head());
+        cp_async_wait_all();
+        __syncthreads();
+        fetch(tile + gridDim.x, s ^ 1);
+        for (int r0 = 0; r0 < n; r0 += groups) {
+            const bool own = r0 + group < n;
+            const int r = own ? r0 + group : n - 1, width = own ? d : 0;
+            const float* st = p.stats + (b * p.L + tile * R + r) * 4;
+            const float mu = st[0], rs = st[1], mu_u = st[2], rs_u = st[3];
+            float D[E], u[E];
+            if (p.dx_out) {
+                bn_gather<E, P>(dxt + r * d, D, g, G, width);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) D[e] = 0.f;
+            }
+            if (p.u) bn_gather<E, P>(ut + r * d, u, g, G, width);
+            if (p.dy) {
+                float v[E], dy[E];
+                float2 sum = make_float2(0.f, 0.f);
+                bn_gather<E, P>(xt + r * d, v, g, G, width);
+                bn_gather<E, P>(dyt + r * d, dy, g, G, width);  // 0 past d, and so is what follows from it
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    v[e] = (v[e] - mu) * rs;
+                    sm[e] = fmaf(own ? dy[e] : 0.f, v[e], sm[e]);
+                    sb[e] += own ? dy[e] : 0.f;
+                    dy[e] *= gamma[e];
+                    sum.x += dy[e];
+                    sum.y = fmaf(dy[e], v[e], sum.y);
+                }
+                sum = bn_group_sum2(sum, G, sh, turn);
+                sum = make_float2(p.rms ? 0.f : sum.x * per, sum.y * per);
+#pragma unroll
+                for (int e = 0; e < E; ++e) D[e] = fmaf(rs, dy[e] - fmaf(v[e], sum.y, sum.x), D[e]);
+            }
+            float o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = p.res_scale * D[e];
+            if (own) bn_scatter<E, P>(xt + r * d, o, g, G, d);
+            if (!p.u) continue;
+            if constexpr (POST) {
+                float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float m = (u[e] - mu_u) * rs_u, q = gate[e] * D[e], w = post_w[e];  // gate, post_w 0 past d
+                    if (own) {
+                        sg[e] = fmaf(D[e], m * w, sg[e]);
+                        sw[e] = fmaf(q, m, sw[e]);
+                    }
+                    t.x = fmaf(q, w, t.x);
+                    t.y = fmaf(q * w, m, t.y);
+                    u[e] = m;
+                    D[e] = q * w;
+                }
+                t = bn_group_sum2(t, G, sh, turn);
+                t = make_float2(p.rms ? 0.f : t.x * per, t.y * per);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = rs_u * (D[e] - fmaf(u[e], t.y, t.x));
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (own) sg[e] = fmaf(D[e], u[e], sg[e]);
+                    o[e] = gate[e] * D[e];
+                }
+            }
+            if (own) bn_scatter<E, P>(ut + r * d, o, g, G, d);
+        }
+        __syncthreads();
+        bn_store_run<TS>(stage, p.dx, rx);
+        if (p.u) bn_store_run<TU>(stage + 2 * xs, p.du, ru);
+    }
+    cp_async_wait_all();
+    if (!p.part) return;
+    // the groups' column sums, in order
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(bn_smem);  // [groups][4][d]
+    bn_scatter<E, P>(sums + (group * 4 + 0) * d, sg, g, G, d);
+    bn_scatter<E, P>(sums + (group * 4 + 1) * d, sw, g, G, d);
+    bn_scatter<E, P>(sums + (group * 4 + 2) * d, sm, g, G, d);
+    bn_scatter<E, P>(sums + (group * 4 + 3) * d, sb, g, G, d);
+    __syncthreads();
+    float* q = p.part + ((int64_t)b * p.nseg + blockIdx.x) * 4 * d;
+    for (int c = threadIdx.x; c < 4 * d; c += blockDim.x) {
+        float t = 0.f;
+        for (int k = 0; k < groups; ++k) t += sums[k * 4 * d + c];
+        q[c] = t;
+    }
+}
+
 // The column sums over the partial rows: of one batch row (blockIdx.z), or
 // of all for the shared vectors.  blockIdx.y: which vector.  A block takes 32
 // columns, each of its warps every sixteenth row; their sums are added in order.

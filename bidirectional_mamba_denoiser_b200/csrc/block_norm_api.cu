@@ -136,29 +136,79 @@ bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
     return one ? launch_run_k<BWD, TS, TU, 1>(k, st, rc) : launch_run_k<BWD, TS, TU, 2>(k, st, rc);
 }
 
+// The packed form: G lanes a row, as few as E elements each allow.
+int pack_lanes(int d, bool bwd) {
+    const int e = bwd ? bimamba::kBnPackBwd : bimamba::kBnPackFwd;
+    int g = 4;
+    while (g * e < d) g *= 2;
+    return g;
+}
+constexpr int kPackMaxD = 4096;  // 512 threads of 8 in the backward
+constexpr size_t kPackSmem = 100 * 1024;
+
+template <bool BWD, typename TS, typename TU, int P>
+int launch_pack_p(BlockNormParams& k, cudaStream_t st) {
+    const int G = pack_lanes(k.d, BWD), threads = std::max(256, G), groups = G > 32 ? 1 : threads / G;
+    const int block = G > 32 ? G : threads, row = k.d * (int)(sizeof(TS) + sizeof(TU)) * (BWD ? 2 : 1);
+    // about 16 KB a stage (24 in the backward), whole rounds of the groups
+    int R = (BWD ? 24576 : 16384) / row / groups * groups;
+    R = (int)std::min<int64_t>(std::max(R, groups), (k.L + groups - 1) / groups * groups);
+    size_t smem = 2 * (size_t)(bimamba::bn_pack_bytes(R, k.d, sizeof(TS)) + bimamba::bn_pack_bytes(R, k.d, sizeof(TU)));
+    if (BWD) smem = std::max(2 * smem, (size_t)groups * 4 * k.d * sizeof(float));
+    void (*fn)(BlockNormParams, int, int);
+    if constexpr (BWD)
+        fn = k.post_w ? bimamba::block_norm_bwd_pack_kernel<TS, TU, P, true>
+                      : bimamba::block_norm_bwd_pack_kernel<TS, TU, P, false>;
+    else
+        fn = k.post_w ? bimamba::block_norm_fwd_pack_kernel<TS, TU, P, true>
+                      : bimamba::block_norm_fwd_pack_kernel<TS, TU, P, false>;
+    if (smem > 2 * kPackSmem) return BIMAMBA_ERR_UNSUPPORTED;  // (no width reaches it)
+    int rc = ensure_smem(reinterpret_cast<const void*>(fn), 2 * kPackSmem);
+    if (rc) return rc;
+    if (!BWD) {
+        const int64_t tiles = (k.L + R - 1) / R;
+        const int held = (int)std::max<size_t>(1, std::min<size_t>(512 / block, 220 * 1024 / (smem + 2048)));
+        k.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)kSms * held / k.batch));
+    }
+    fn<<<dim3((unsigned)k.nseg, (unsigned)k.batch), block, smem, st>>>(k, G, R);
+    return launch_status();
+}
+
+template <bool BWD, typename TS, typename TU>
+int launch_pack(BlockNormParams& k, cudaStream_t st) {
+    return k.d % 2 ? launch_pack_p<BWD, TS, TU, 1>(k, st) : launch_pack_p<BWD, TS, TU, 2>(k, st);
+}
+
+// Which form.  The copying one where a row fills a warp and is whole groups of
+// eight; the packed one for other rows up to kPackMaxD columns; the plain one for wider
+// odd rows, for pointers that no 16-byte access can use, and for batch rows
+// of a few tokens that have vectors of their own (a block a batch row would
+// be idle).
 template <bool BWD>
-int launch(BlockNormParams& k, bool vec, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
-    // its fp32 stores are of 32 bytes
+int launch(BlockNormParams& k, bool vec, bool chunks, bimamba_dtype_t ts, bimamba_dtype_t tu, cudaStream_t st) {
+    // the copying form's fp32 stores are of 32 bytes
     const bool wide = (ts == BIMAMBA_BF16 || (aligned(k.x_out, 32) && aligned(k.dx, 32))) &&
                       (tu == BIMAMBA_BF16 || (aligned(k.y, 32) && aligned(k.du, 32)));
-    if (vec && wide && k.d >= 256 && k.d <= 16 * bimamba::kBlockNormThreads) {  // narrower rows would not fill a warp
+    if (vec && wide && k.d >= 256 && k.d <= 16 * bimamba::kBlockNormThreads) {
         int rc = BIMAMBA_OK;
         if (ts == BIMAMBA_BF16 ? launch_run<BWD, bf16, bf16>(k, st, rc)
                                : (tu == BIMAMBA_BF16 ? launch_run<BWD, float, bf16>(k, st, rc)
                                                      : launch_run<BWD, float, float>(k, st, rc)))
             return rc;
     }
+    if (chunks && k.d <= kPackMaxD && (k.L >= 16 || k.batch == 1)) {
+        if (ts == BIMAMBA_BF16) return launch_pack<BWD, bf16, bf16>(k, st);
+        return tu == BIMAMBA_BF16 ? launch_pack<BWD, float, bf16>(k, st) : launch_pack<BWD, float, float>(k, st);
+    }
     return launch_rows<BWD>(k, shape_for(k.d, vec), ts, tu, st);
 }
 
 // Row segments of the backward per batch row, each with its own column sums:
-// one for each block (128 registers a thread) or warp that the SMs hold, but at
-// least 8 rows a segment.
+// one for each block that the SMs hold (128 registers a thread), but at least
+// 8 rows a segment.
 int segments(int batch, int64_t L, int d) {
-    const bool copying = d % 8 == 0 && d >= 256;
-    const int groups = d % 8 ? d : d / 8;
-    const int held = copying ? std::max(1, std::min(16, 512 / std::min(512, (groups + 31) / 32 * 32)))
-                             : (groups <= 128 ? 16 : 1);
+    const int threads = d % 8 == 0 && d >= 256 ? std::min(512, (d / 8 + 31) / 32 * 32) : std::max(256, pack_lanes(d, true));
+    const int held = std::max(1, std::min(16, 512 / threads));
     const int64_t want = std::max<int64_t>(1, (int64_t)held * kSms / batch), most = std::max<int64_t>(1, L / 8);
     return (int)std::min(want, most);
 }
@@ -192,8 +242,11 @@ int bimamba_block_norm_fwd(const void* x, const void* u, const bimamba_block_nor
     k.x_out = x_out;
     k.y = y;
     k.stats = stats;
-    const bool vec = d % 8 == 0 && all_aligned16(x, u, x_out, y, stats, p->gate, p->post_w, p->gamma, p->beta);
-    return launch<false>(k, vec, stream_dtype, dtype, static_cast<cudaStream_t>(cuda_stream));
+    const bool chunks = all_aligned16(x, u, x_out, y);
+    const bool vec = chunks && d % 8 == 0 && all_aligned16(stats, p->gate, p->post_w, p->gamma, p->beta);
+    // vectors that all rows share make the batch one long row
+    if ((!k.gate || !k.gate_bs) && ((!k.gamma && !k.beta) || !k.gamma_bs)) k.L *= batch, k.batch = 1;
+    return launch<false>(k, vec, chunks, stream_dtype, dtype, static_cast<cudaStream_t>(cuda_stream));
 }
 
 size_t bimamba_block_norm_workspace_bytes(int batch, int64_t L, int d) {
@@ -234,10 +287,10 @@ int bimamba_block_norm_bwd(const void* dy, const void* dx_out, const void* x_out
     k.nseg = segments(batch, L, d);
     const bool sums = g->dgate || g->dpost_w || g->dgamma || g->dbeta;
     k.part = sums ? static_cast<float*>(workspace) : nullptr;
-    const bool vec = d % 8 == 0 && all_aligned16(dy, dx_out, x_out, u, (const void*)g->dx, (const void*)g->du, stats,
-                                                 p->gate, p->post_w, p->gamma);
+    const bool chunks = all_aligned16(dy, dx_out, x_out, u, (const void*)g->dx, (const void*)g->du);
+    const bool vec = chunks && d % 8 == 0 && all_aligned16(stats, p->gate, p->post_w, p->gamma);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    if ((rc = launch<true>(k, vec, stream_dtype, dtype, st)) || !sums) return rc;
+    if ((rc = launch<true>(k, vec, chunks, stream_dtype, dtype, st)) || !sums) return rc;
     const dim3 grid((unsigned)((d + 31) / 32), 4, (unsigned)batch);
     bimamba::block_norm_sums_kernel<<<grid, 32 * bimamba::kBnSumWarps, 0, st>>>(
         k.part, k.nseg, batch, d, g->dgate, g->dpost_w, g->dgamma, g->dbeta, (flags & BIMAMBA_NORM_GATE_SHARED) != 0,
