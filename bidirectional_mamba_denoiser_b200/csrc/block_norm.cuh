@@ -417,12 +417,15 @@ __device__ __forceinline__ void bn_share(BnShared& sh, float columns) {
 }
 // The block's sums of a pair.
 __device__ __forceinline__ float2 bn_block_sum2(float2 v, BnShared& sh, int& turn) {
-    v = make_float2(bn_warp_sum(v.x), bn_warp_sum(v.y));
-    const int nw = blockDim.x >> 5;
-    if (nw == 1) return v;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    // even lanes take x over, odd ones y: one shuffle a step for both
+    float t = (lane & 1 ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, lane & 1 ? v.x : v.y, 1);
+#pragma unroll
+    for (int off = 2; off <= 16; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (nw == 1) return make_float2(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 1));
     float4* r = sh.part[turn];
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(r)[threadIdx.x >> 5] = v;
+    if (lane < 2) reinterpret_cast<float*>(r)[(threadIdx.x >> 5) * 2 + lane] = t;
     __syncthreads();
     v = make_float2(0.f, 0.f);
 #pragma unroll
@@ -504,8 +507,8 @@ template <typename TS, typename TU>
 constexpr int kBnFwdStages = sizeof(TU) == 4 ? 3 : 4;
 template <typename TS, typename TU, int K>
 constexpr int kBnFwdPieces = K * (kBnPieces<TS> + kBnPieces<TU>);
-template <int K>
-constexpr int kBnBwdStages = K == 1 ? 4 : 2;
+template <typename TU, int K>
+constexpr int kBnBwdStages = K == 1 ? 4 : (sizeof(TU) == 4 ? 1 : 2);
 template <typename TS, typename TU, int K>
 constexpr int kBnBwdPieces = K * 2 * (kBnPieces<TS> + kBnPieces<TU>);
 
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__(kBlockNormThreads) block_norm_fwd_run_kernel(c
 
 template <typename TS, typename TU, int K, bool POST>
 __global__ void __launch_bounds__(kBlockNormThreads) block_norm_bwd_run_kernel(const BlockNormParams p) {
-    constexpr int NS = kBnBwdStages<K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
+    constexpr int NS = kBnBwdStages<TU, K>, PIECES = kBnBwdPieces<TS, TU, K>, PS = kBnPieces<TS>, PU = kBnPieces<TU>;
     extern __shared__ __align__(16) unsigned char bn_smem[];
     __shared__ BnShared sh;
     int turn = 0;

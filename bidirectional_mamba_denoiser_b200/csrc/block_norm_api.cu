@@ -105,7 +105,7 @@ int run_threads(int d, int k) { return ((d / 8 + k - 1) / k + 31) / 32 * 32; }
 template <bool BWD, typename TS, typename TU, int K>
 bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     constexpr int pieces = BWD ? bimamba::kBnBwdPieces<TS, TU, K> : bimamba::kBnFwdPieces<TS, TU, K>;
-    constexpr int stages = BWD ? bimamba::kBnBwdStages<K> : bimamba::kBnFwdStages<TS, TU>;
+    constexpr int stages = BWD ? bimamba::kBnBwdStages<TU, K> : bimamba::kBnFwdStages<TS, TU>;
     const int threads = run_threads(k.d, K);
     const size_t smem = (size_t)stages * pieces * threads * 16;
     if (smem > kMaxRunSmem) return false;
@@ -118,8 +118,8 @@ bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
                       : bimamba::block_norm_fwd_run_kernel<TS, TU, K, false>;
     // one limit for all widths: it is raised once a kernel
     if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), kMaxRunSmem))) return true;
-    if (!BWD) {  // one run a block that an SM holds
-        const int held = (int)std::min<size_t>(std::min(512 / threads, 16), 220 * 1024 / (smem + 2048));
+    if (!BWD) {  // one run a block that an SM holds (up to 96 registers a thread, 128 for K = 2)
+        const int held = (int)std::min<size_t>(std::min((K == 1 ? 640 : 512) / threads, 24), 220 * 1024 / (smem + 2048));
         k.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(k.L, (int64_t)kSms * std::max(held, 1) / k.batch));
     }
     fn<<<dim3((unsigned)k.nseg, (unsigned)k.batch), threads, smem, st>>>(k);
@@ -132,7 +132,7 @@ bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
 // backward's column sums leave room for one, up to 512 threads.
 template <bool BWD, typename TS, typename TU>
 bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
-    const bool one = BWD ? k.d <= 8 * bimamba::kBlockNormThreads : k.d < 1024;
+    const bool one = BWD ? k.d <= 8 * bimamba::kBlockNormThreads : k.d <= 256;
     return one ? launch_run_k<BWD, TS, TU, 1>(k, st, rc) : launch_run_k<BWD, TS, TU, 2>(k, st, rc);
 }
 
@@ -140,8 +140,8 @@ bool launch_run(BlockNormParams& k, cudaStream_t st, int& rc) {
 int pack_lanes(int d, bool bwd) {
     const int e = bwd ? bimamba::kBnPackBwd : bimamba::kBnPackFwd;
     int g = 4;
-    while (g * e < d) g *= 2;
-    return g;
+    while (g < 32 && g * e < d) g *= 2;
+    return g * e < d ? (d + 32 * e - 1) / (32 * e) * 32 : g;
 }
 constexpr int kPackMaxD = 4096;  // 512 threads of 8 in the backward
 constexpr size_t kPackSmem = 100 * 1024;
