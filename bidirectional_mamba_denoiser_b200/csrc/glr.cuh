@@ -39,6 +39,12 @@ struct GlrRows {
 };
 enum { kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ, kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors };
 
+constexpr int kGlrByMap = 64;
+// Maps of the inputs, kGlrR to kGlrZ: [batch][L][D], boxes of one warp's rows.
+struct GlrMaps {
+    CUtensorMap m[kGlrZ + 1];
+};
+
 struct GlrParams {
     GlrRows rows[kGlrTensors];  // p null where the call has none
     const float* A;
@@ -53,7 +59,7 @@ struct GlrParams {
     float* part;           // backward: [batch * nchunk][3][D] partial sums
     int64_t L;
     int D, batch, reverse;
-    int copy;              // bytes of one asynchronous copy: 16, a pair of elements, or 0 (none possible)
+    int copy;              // kGlrByMap, or the bytes of one cp.async: 16, a pair of elements, 0 (none possible)
     int64_t nchunk;        // ceil(L / kGlrChunk)
 };
 
@@ -230,9 +236,11 @@ __device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
 //
 // Blocks stay (as many as the GPU holds) and take the next tile's ticket while
 // they work on one.  Each warp copies the rows of its own steps into its own
-// part of shared memory (cp.async, 16 bytes a lane), NS tiles ahead, so the
-// copies overlap the arithmetic without a barrier: a warp waits for its own
-// copies only.
+// part of shared memory, NS tiles ahead, so the copies overlap the arithmetic
+// without a block barrier: a warp waits for its own copies only.  Long calls
+// copy by tensor maps, one box a tensor that one lane asks for (in reverse the
+// box's rows are the steps backwards); others by cp.async, whose addresses cost
+// the warp some 20 instructions a tensor.
 constexpr int kGlrSlab = 64;
 constexpr int kGlrGroup = 8;
 static_assert(kGlrGroup == 8, "a piece for each warp");
@@ -566,17 +574,59 @@ __device__ __forceinline__ void glr_copy_rows(T* to, const GlrParams& p, const G
     };
     (one(TENSORS), ...);
 }
-// Steps past a warp's last keep the state: their rows (zeros so far) get a
-// closed gate r = -inf, so that a = 1 and w = 0 without a select in the scan.
-template <typename T, int TOK>
-__device__ __forceinline__ void glr_close_rows(T* r, int n) {
-    const int lane = threadIdx.x & 31;
-    for (int j = n; j < TOK; ++j) {
-        if constexpr (sizeof(T) == 2)
-            reinterpret_cast<uint32_t*>(r + j * kGlrSlab)[lane] = 0xff80ff80u;
-        else
-            reinterpret_cast<uint2*>(r + j * kGlrSlab)[lane] = make_uint2(0xff800000u, 0xff800000u);
+// The same by maps, from step `first` of the row on, completing on `bar`; a
+// warp without steps completes it with nothing.
+template <typename T, int TOK, int... TENSORS>
+__device__ __forceinline__ void glr_copy_boxes(T* to, const GlrMaps& maps, const GlrParams& p, const GlrTile& t,
+                                               int64_t first, int n, int c, uint64_t* bar) {
+    if ((threadIdx.x & 31) != 0) return;
+    if (n == 0) {
+        mbar_arrive(bar);
+        return;
     }
+    constexpr int BYTES = TOK * kGlrSlab * (int)sizeof(T);
+    mbar_arrive_expect_tx(bar, ((p.rows[TENSORS].p ? BYTES : 0) + ...));
+    const int t0 = (int)(p.reverse ? t.len - first - TOK : first);  // below 0: zeros
+    const auto one = [&](int tensor) {
+        if (p.rows[tensor].p) tma_load_3d(to, &maps.m[tensor], bar, c, t0, t.b);
+        to += TOK * kGlrSlab;
+    };
+    (one(TENSORS), ...);
+}
+// Bounded, like every wait.
+__device__ __forceinline__ void glr_wait_boxes(uint64_t* bar, unsigned parity) {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > 4000000000LL) {
+            atomicOr(&g_glr_error, kErrTmaTimeout);
+            return;
+        }
+    }
+}
+
+// Where the row of a warp's step j lies.  BACK: a reverse call by maps, the rows
+// of a box run with the tokens.
+template <int TOK, bool BACK>
+struct GlrOrder {
+    __device__ __forceinline__ constexpr int operator()(int j) const { return (BACK ? TOK - 1 - j : j) * kGlrSlab; }
+};
+
+// Steps past a warp's last keep the state: their rows in all NT tensors become
+// zeros, but r = -inf, a closed gate, so that a = 1 and w = 0 without a select
+// in the scan.
+template <typename T, int TOK, int NT, bool BACK>
+__device__ __forceinline__ void glr_close_rows(T* rows, GlrOrder<TOK, BACK> at, int n) {
+    const int lane = threadIdx.x & 31;
+    for (int j = n; j < TOK; ++j)
+        for (int q = 0; q < NT; ++q) {
+            T* const to = rows + q * TOK * kGlrSlab + at(j);
+            if constexpr (sizeof(T) == 2)
+                reinterpret_cast<uint32_t*>(to)[lane] = q == 0 ? 0xff80ff80u : 0u;
+            else
+                reinterpret_cast<uint2*>(to)[lane] = q == 0 ? make_uint2(0xff800000u, 0xff800000u) : make_uint2(0u, 0u);
+        }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a box may overwrite them
 }
 // -bias log2 e and A log2 e of a pair, kept finite so that a closed gate wins.
 __device__ __forceinline__ float2 glr_finite(float2 v) {
@@ -586,14 +636,14 @@ template <bool VEC>
 __device__ __forceinline__ float2 glr_scaled(const float* v, int c, int nch, float by) {
     return glr_finite(glr_mul(glr_vec2<VEC>(v, c, nch), glr_f2(by)));
 }
-// The lane's pair of row j, and its negative.
+// The lane's pair of a row, and its negative.
 template <typename T>
-__device__ __forceinline__ float2 glr_minus_row(const T* rows, int j) {
-    return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].neg();
+__device__ __forceinline__ float2 glr_minus_row(const T* row) {
+    return reinterpret_cast<const GlrRaw<T>*>(row)[threadIdx.x & 31].neg();
 }
 template <typename T>
-__device__ __forceinline__ float2 glr_row(const T* rows, int j) {
-    return reinterpret_cast<const GlrRaw<T>*>(rows + j * kGlrSlab)[threadIdx.x & 31].get();
+__device__ __forceinline__ float2 glr_row(const T* row) {
+    return reinterpret_cast<const GlrRaw<T>*>(row)[threadIdx.x & 31].get();
 }
 
 // EPI: 0 out = h, 1 with add, 2 with z (an absent add is zero rows).
@@ -603,29 +653,42 @@ constexpr int kGlrFwdStages = EPI ? 1 : 2;
 template <typename T, int EPI>
 constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + EPI) * kGlrTok<T> * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, int EPI>
+template <typename T, bool VEC, int EPI, bool BACK>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
-    glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y) {
+    glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrTok<T>, NS = kGlrFwdStages<EPI>, ROWS = TOK * kGlrSlab;
-    extern __shared__ __align__(16) unsigned char glr_smem[];
+    extern __shared__ __align__(128) unsigned char glr_smem[];
     __shared__ float4 aggs[2][kGlrWarps][32];      // (P, h) of each warp
     __shared__ float4 pieces[2][kGlrGroup][32];    // what glr_ask fetched; [7] the state entering the group (or the row)
     __shared__ GlrEntry queue[kGlrQueue];
+    __shared__ uint64_t bars[kGlrWarps][NS + 1];  // a warp's stages, and its add and z
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrFwdWarpBytes<T, EPI>);
     T* const epi = mine + 3 * NS * ROWS;  // z, then add
     const int tile_steps = nwarp * TOK;
+    const bool by_map = p.copy == kGlrByMap;
+    constexpr GlrOrder<TOK, BACK> at;
+    uint64_t* const bar = bars[warp];
 
     auto copy_inputs = [&](const GlrEntry& e, int stage) {
         const GlrTile t = e.t;
-        const int n = t.at < 0 ? 0 : glr_steps(t.len, (int64_t)t.at * tile_steps + warp * TOK, TOK);
-        if (n) {
+        const int64_t ws = (int64_t)t.at * tile_steps + warp * TOK;
+        const int n = t.at < 0 ? 0 : glr_steps(t.len, ws, TOK);
+        if (by_map) {
+            glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, maps, p, t, ws, n, glr_channel(p, t),
+                                                        bar + stage);
+        } else if (n) {
             const int left = p.D - glr_channel(p, t);
             glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, p, e, warp * TOK, n, left);
         }
         cp_async_commit();
     };
 
+    if (by_map && threadIdx.x == 0) {
+        for (int w = 0; w < nwarp; ++w)
+            for (int k = 0; k <= NS; ++k) mbar_init(&bars[w][k], 1);
+        fence_barrier_init();
+    }
     GlrQueue<false, sizeof(T)> tiles{queue, tile_steps};
     tiles.start(p, y, NS);
     if (EPI == 2 && !p.rows[kGlrAdd].p) {
@@ -650,8 +713,13 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         float4(*got)[32] = pieces[k & 1];
         float2 Ps[TOK], hs[TOK];
         cp_async_wait_pending<NS - 1>();
+        if (by_map) glr_wait_boxes(bar + stage, (k / NS) & 1);
         __syncwarp();
-        if constexpr (EPI > 0) {
+        if (EPI > 0 && by_map) {
+            const int c = c0 - 2 * lane;
+            if constexpr (EPI == 1) glr_copy_boxes<T, TOK, kGlrAdd>(epi, maps, p, t, ws, n, c, bar + NS);
+            if constexpr (EPI == 2) glr_copy_boxes<T, TOK, kGlrZ, kGlrAdd>(epi, maps, p, t, ws, n, c, bar + NS);
+        } else if constexpr (EPI > 0) {
             // every lane is past its last tile's outputs
             const int left = p.D - (c0 - 2 * lane);
             if (EPI == 2 && n) glr_copy_rows<T, TOK, kGlrZ>(epi, p, e, warp * TOK, n, left);
@@ -661,15 +729,15 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         if (n) {
             T* in = mine + stage * 3 * ROWS;
-            if (n < TOK) glr_close_rows<T, TOK>(in, n);
+            if (n < TOK) glr_close_rows<T, TOK, 3, BACK>(in, at, n);
             const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
             float2 P = glr_f2(1.f), h = glr_f2(0.f);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
-                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, nA2);
-                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in + 2 * ROWS, j));
+                const GlrGate2 g = glr_gate2(glr_row(in + at(j)), glr_row(in + ROWS + at(j)), nr, ni, nA2);
+                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in + 2 * ROWS + at(j)));
                 P = glr_mul(P, g.a);
                 h = glr_fma(g.a, h, w);
                 Ps[j] = P;
@@ -718,6 +786,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             glr_st2<VEC>(p.chunk + ((int64_t)t.b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
         if constexpr (EPI > 0) {
             cp_async_wait_pending<1>();  // all but the next tile's inputs
+            if (by_map) glr_wait_boxes(bar + NS, k & 1);
             __syncwarp();
         }
         const int64_t ts = p.rows[kGlrOut].ts;
@@ -726,9 +795,9 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 float2 h = glr_fma(Ps[j], c, hs[j]);
-                if constexpr (EPI > 0) h = glr_add(h, glr_row(epi + (EPI - 1) * ROWS, j));
+                if constexpr (EPI > 0) h = glr_add(h, glr_row(epi + (EPI - 1) * ROWS + at(j)));
                 if constexpr (EPI == 2) {
-                    const float2 z = glr_row(epi, j);
+                    const float2 z = glr_row(epi + at(j));
                     h = glr_mul(h, glr_mul(z, glr_sigmoid2(z)));
                 }
                 if (decltype(full)::value || j < n) glr_st2<VEC>(reinterpret_cast<T*>(po), h, nch);
@@ -757,25 +826,37 @@ constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
 template <typename T, int EPI>
 constexpr int kGlrBwdWarpBytes = (EPI == 2 ? 6 : 4) * kGlrBwdStages<T> * kGlrBwdTok * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, int EPI>
+template <typename T, bool VEC, int EPI, bool BACK>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
-    glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y) {
+    glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI == 2 ? 6 : 4;
-    extern __shared__ __align__(16) unsigned char glr_smem[];
+    extern __shared__ __align__(128) unsigned char glr_smem[];
     __shared__ float4 agg[kGlrWarps][32];   // (P, q) of each warp
     __shared__ float2 aggh[kGlrWarps][32];  // its h
     __shared__ float4 pieces[kGlrGroup][32];
     __shared__ float2 sums[3][kGlrWarps][32];
     __shared__ GlrEntry queue[kGlrQueue];
+    __shared__ uint64_t bars[kGlrWarps][NS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrBwdWarpBytes<T, EPI>);
 
+    const bool by_map = p.copy == kGlrByMap;
+    constexpr GlrOrder<TOK, BACK> at;
+    uint64_t* const bar = bars[warp];
+
     auto copy_inputs = [&](const GlrEntry& e, int stage) {
         const GlrTile t = e.t;
-        const int n = t.at < 0 ? 0 : glr_steps(t.len, glr_first_step<true>(t, kGlrChunk) + warp * TOK, TOK);
-        if (n) {
+        const int64_t ws = glr_first_step<true>(t, kGlrChunk) + warp * TOK;
+        const int n = t.at < 0 ? 0 : glr_steps(t.len, ws, TOK);
+        T* to = mine + stage * NT * ROWS;
+        if (by_map) {
+            const int c = glr_channel(p, t);
+            if constexpr (EPI == 2)
+                glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ, kGlrAdd>(to, maps, p, t, ws, n, c, bar + stage);
+            else
+                glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout>(to, maps, p, t, ws, n, c, bar + stage);
+        } else if (n) {
             const int left = p.D - glr_channel(p, t);
-            T* to = mine + stage * NT * ROWS;
             if constexpr (EPI == 2) {
                 glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ>(to, p, e, warp * TOK, n, left);
                 if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK, kGlrAdd>(to + 5 * ROWS, p, e, warp * TOK, n, left);
@@ -797,6 +878,11 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
     };
 
+    if (by_map && threadIdx.x == 0) {
+        for (int w = 0; w < kGlrWarps; ++w)
+            for (int k = 0; k < NS; ++k) mbar_init(&bars[w][k], 1);
+        fence_barrier_init();
+    }
     GlrQueue<true, sizeof(T)> tiles{queue, kGlrChunk};
     tiles.start(p, y, NS);
     if (EPI == 2 && !p.rows[kGlrAdd].p) {
@@ -823,17 +909,18 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         float2 nrg[TOK], nig[TOK], nu[TOK], hp[TOK];
         const float2 entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
         cp_async_wait_pending<NS - 1>();
+        if (by_map) glr_wait_boxes(bar + stage, (k / NS) & 1);
         __syncwarp();
         float2 P = glr_f2(1.f), q = glr_f2(0.f), h = glr_f2(0.f);
         if (n) {
-            if (n < TOK) glr_close_rows<T, TOK>(in, n);
+            if (n < TOK) glr_close_rows<T, TOK, NT, BACK>(in, at, n);
             const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
-                const GlrGate2 g = glr_gate2(glr_row(in, j), glr_row(in + ROWS, j), nr, ni, nA2);
-                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in_x, j));
+                const GlrGate2 g = glr_gate2(glr_row(in + at(j)), glr_row(in + ROWS + at(j)), nr, ni, nA2);
+                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in_x + at(j)));
                 nrg[j] = g.nrg;
                 nig[j] = make_float2(glr_rcp(-g.di.x), glr_rcp(-g.di.y));
                 nu[j] = g.nu;
@@ -843,9 +930,9 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             }
 #pragma unroll
             for (int j = TOK - 1; j >= 0; --j) {
-                float2 dh = glr_row(in_d, j);
+                float2 dh = glr_row(in_d + at(j));
                 if constexpr (EPI == 2) {
-                    const float2 z = glr_row(in_z, j);
+                    const float2 z = glr_row(in_z + at(j));
                     dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
                 }
                 const float2 G = glr_add(q, dh);
@@ -927,14 +1014,14 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                 // 1 / beta
                 const float2 rb = make_float2(glr_rsqrt(kGlrTiny - nb2.x), glr_rsqrt(kGlrTiny - nb2.y));
                 const float2 bi = glr_mul(glr_mul(nb2, rb), nig[j]);  // beta ig
-                const float2 w = glr_mul(bi, glr_row(in_x, j));
+                const float2 w = glr_mul(bi, glr_row(in_x + at(j)));
                 const float2 h = glr_add(glr_fma(nu[j], hp[j], hp[j]), w);
-                float2 dh = glr_row(in_d, j);
+                float2 dh = glr_row(in_d + at(j));
                 if constexpr (EPI == 2) {
-                    const float2 z = glr_row(in_z, j), sz = glr_sigmoid2(z);
+                    const float2 z = glr_row(in_z + at(j)), sz = glr_sigmoid2(z);
                     // silu'(z) = s (1 + z (1 - s))
                     const float2 ds = glr_fma(glr_mul(sz, z), make_float2(1.f - sz.x, 1.f - sz.y), sz);
-                    put(kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add, j))), ds));
+                    put(kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add + at(j)))), ds));
                     dh = glr_mul(dh, glr_mul(z, sz));
                 }
                 if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);

@@ -175,8 +175,41 @@ bool pairs(const GlrParams& k, int esz) {
     return k.D % 2 == 0 && starts_at(k, bimamba::kGlrOut, bimamba::kGlrDz, 2 * esz);
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Maps of the inputs that the call has; false where one cannot be mapped
+// (rows shared by tokens or by the batch).
+bool make_maps(bimamba::GlrMaps& maps, const GlrParams& k, int esz, int rows) {
+    static const EncodeFn encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    if (!encode) return false;
+    for (int q = bimamba::kGlrR; q <= bimamba::kGlrZ; ++q) {
+        const GlrRows& r = k.rows[q];
+        if (!r.p) continue;
+        const int64_t ts = r.ts < 0 ? -(int64_t)r.ts : r.ts, bs = k.batch > 1 ? r.bs : ts * k.L;
+        if (ts <= 0 || bs <= 0 || bs >= (1LL << 40)) return false;
+        const cuuint64_t dims[3] = {(cuuint64_t)k.D, (cuuint64_t)k.L, (cuuint64_t)k.batch};
+        const cuuint64_t strides[2] = {(cuuint64_t)ts, (cuuint64_t)bs};
+        const cuuint32_t box[3] = {(cuuint32_t)bimamba::kGlrSlab, (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
+        if (encode(&maps.m[q], esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, r.p, dims,
+                   strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    return true;
+}
+
 // Blocks that stay: what the SMs hold at 128 registers a thread.
-int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, int64_t tiles, int tile_steps, int warps,
+using TilesFn = void (*)(GlrParams, bimamba::GlrSync, bimamba::GlrMaps);
+int launch_tiles(TilesFn fn, TilesFn back, GlrParams& k, int esz, int64_t tiles, int tile_steps, int warps,
                  size_t warp_bytes, unsigned flags, void* ws, cudaStream_t st) {
     const int64_t total = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
     // tickets run past the total by what the blocks take ahead
@@ -186,31 +219,41 @@ int launch_tiles(void (*fn)(GlrParams, bimamba::GlrSync), const GlrParams& k, in
     if (rc) return rc;
     y.total = (unsigned)total;
     const size_t smem = warps * warp_bytes;
-    if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), bimamba::kGlrWarps * warp_bytes))) return rc;
     constexpr size_t kFixed = 17 * 1024 + 1024;  // static shared memory and the 1 KB that the system keeps
     const int by_regs = 16 / warps, by_smem = (int)(228 * 1024 / (smem + kFixed));
     const int64_t held = (int64_t)kSms * std::max(1, std::min(by_regs, by_smem));
-    fn<<<(unsigned)std::min(total, held), warps * 32, smem, st>>>(k, y);
+    // maps take the host some microseconds: where every block has several tiles
+    bimamba::GlrMaps maps = {};
+    if (back && k.copy == 16 && total >= 4 * held && make_maps(maps, k, esz, tile_steps / bimamba::kGlrWarps)) {
+        k.copy = bimamba::kGlrByMap;
+        if (k.reverse) fn = back;
+    }
+    if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), bimamba::kGlrWarps * warp_bytes))) return rc;
+    fn<<<(unsigned)std::min(total, held), warps * 32, smem, st>>>(k, y, maps);
     return launch_status();
 }
 
 template <typename T, bool VEC, int EPI>
-int launch_fwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+int launch_fwd_epi(GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
     const int64_t tiles = (k.L + TILE - 1) / TILE;
     const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
-    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI>, k, tiles, TILE, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
+    TilesFn back = nullptr;  // (16-byte copies of the inputs come with paired outputs as good as always)
+    if constexpr (VEC) back = bimamba::glr_tile_fwd_kernel<T, VEC, EPI, true>;
+    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI, false>, back, k, (int)sizeof(T), tiles, TILE, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
                         flags, ws, st);
 }
 
 template <typename T, bool VEC, int EPI>
-int launch_bwd_epi(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
-    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI>, k, k.nchunk, bimamba::kGlrChunk, bimamba::kGlrWarps,
+int launch_bwd_epi(GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+    TilesFn back = nullptr;
+    if constexpr (VEC) back = bimamba::glr_tile_bwd_kernel<T, VEC, EPI, true>;
+    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI, false>, back, k, (int)sizeof(T), k.nchunk, bimamba::kGlrChunk, bimamba::kGlrWarps,
                         bimamba::kGlrBwdWarpBytes<T, EPI>, flags, ws, st);
 }
 
 template <bool BWD, typename T, bool VEC>
-int launch_vec(const GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
+int launch_vec(GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     const int epi = k.rows[bimamba::kGlrZ].p ? 2 : (k.rows[bimamba::kGlrAdd].p ? 1 : 0);
     if constexpr (BWD) {
         if (epi == 2) return launch_bwd_epi<T, VEC, 2>(k, flags, ws, st);
