@@ -39,7 +39,6 @@ struct GlrRows {
 };
 enum { kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ, kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors };
 
-constexpr int kGlrByMap = 64;
 // Maps of the inputs, kGlrR to kGlrZ: [batch][L][D], boxes of one warp's rows.
 struct GlrMaps {
     CUtensorMap m[kGlrZ + 1];
@@ -59,7 +58,7 @@ struct GlrParams {
     float* part;           // backward: [batch * nchunk][3][D] partial sums
     int64_t L;
     int D, batch, reverse;
-    int copy;              // kGlrByMap, or the bytes of one cp.async: 16, a pair of elements, 0 (none possible)
+    int copy;              // bytes of one cp.async: 16, a pair of elements, or 0 (none possible)
     int64_t nchunk;        // ceil(L / kGlrChunk)
 };
 
@@ -605,18 +604,21 @@ __device__ __forceinline__ void glr_wait_boxes(uint64_t* bar, unsigned parity) {
     }
 }
 
-// Where the row of a warp's step j lies.  BACK: a reverse call by maps, the rows
-// of a box run with the tokens.
-template <int TOK, bool BACK>
+// How a kernel's inputs come: by cp.async, or by maps forward or in reverse.
+enum { kGlrAsync, kGlrMapForward, kGlrMapReverse };
+// Where the row of a warp's step j lies: the rows of a box run with the tokens.
+template <int TOK, int MODE>
 struct GlrOrder {
-    __device__ __forceinline__ constexpr int operator()(int j) const { return (BACK ? TOK - 1 - j : j) * kGlrSlab; }
+    __device__ __forceinline__ constexpr int operator()(int j) const {
+        return (MODE == kGlrMapReverse ? TOK - 1 - j : j) * kGlrSlab;
+    }
 };
 
 // Steps past a warp's last keep the state: their rows in all NT tensors become
 // zeros, but r = -inf, a closed gate, so that a = 1 and w = 0 without a select
 // in the scan.
-template <typename T, int TOK, int NT, bool BACK>
-__device__ __forceinline__ void glr_close_rows(T* rows, GlrOrder<TOK, BACK> at, int n) {
+template <typename T, int TOK, int NT, int MODE>
+__device__ __forceinline__ void glr_close_rows(T* rows, GlrOrder<TOK, MODE> at, int n) {
     const int lane = threadIdx.x & 31;
     for (int j = n; j < TOK; ++j)
         for (int q = 0; q < NT; ++q) {
@@ -653,7 +655,7 @@ constexpr int kGlrFwdStages = EPI ? 1 : 2;
 template <typename T, int EPI>
 constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + EPI) * kGlrTok<T> * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, int EPI, bool BACK>
+template <typename T, bool VEC, int EPI, int MODE>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
     glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrTok<T>, NS = kGlrFwdStages<EPI>, ROWS = TOK * kGlrSlab;
@@ -666,22 +668,22 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrFwdWarpBytes<T, EPI>);
     T* const epi = mine + 3 * NS * ROWS;  // z, then add
     const int tile_steps = nwarp * TOK;
-    const bool by_map = p.copy == kGlrByMap;
-    constexpr GlrOrder<TOK, BACK> at;
+    constexpr bool by_map = MODE != kGlrAsync;
+    constexpr GlrOrder<TOK, MODE> at;
     uint64_t* const bar = bars[warp];
 
     auto copy_inputs = [&](const GlrEntry& e, int stage) {
         const GlrTile t = e.t;
         const int64_t ws = (int64_t)t.at * tile_steps + warp * TOK;
         const int n = t.at < 0 ? 0 : glr_steps(t.len, ws, TOK);
-        if (by_map) {
+        if constexpr (by_map) {
             glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, maps, p, t, ws, n, glr_channel(p, t),
                                                         bar + stage);
-        } else if (n) {
+        } else {
             const int left = p.D - glr_channel(p, t);
-            glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, p, e, warp * TOK, n, left);
+            if (n) glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX>(mine + stage * 3 * ROWS, p, e, warp * TOK, n, left);
+            cp_async_commit();
         }
-        cp_async_commit();
     };
 
     if (by_map && threadIdx.x == 0) {
@@ -712,10 +714,12 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         float4(*agg)[32] = aggs[k & 1];
         float4(*got)[32] = pieces[k & 1];
         float2 Ps[TOK], hs[TOK];
-        cp_async_wait_pending<NS - 1>();
-        if (by_map) glr_wait_boxes(bar + stage, (k / NS) & 1);
+        if constexpr (by_map)
+            glr_wait_boxes(bar + stage, (k / NS) & 1);
+        else
+            cp_async_wait_pending<NS - 1>();
         __syncwarp();
-        if (EPI > 0 && by_map) {
+        if constexpr (EPI > 0 && by_map) {
             const int c = c0 - 2 * lane;
             if constexpr (EPI == 1) glr_copy_boxes<T, TOK, kGlrAdd>(epi, maps, p, t, ws, n, c, bar + NS);
             if constexpr (EPI == 2) glr_copy_boxes<T, TOK, kGlrZ, kGlrAdd>(epi, maps, p, t, ws, n, c, bar + NS);
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         if (n) {
             T* in = mine + stage * 3 * ROWS;
-            if (n < TOK) glr_close_rows<T, TOK, 3, BACK>(in, at, n);
+            if (n < TOK) glr_close_rows<T, TOK, 3, MODE>(in, at, n);
             const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);
@@ -785,8 +789,10 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if (p.chunk && n > 0 && ws % kGlrChunk == 0)
             glr_st2<VEC>(p.chunk + ((int64_t)t.b * p.nchunk + ws / kGlrChunk) * p.D + c0, c, nch);
         if constexpr (EPI > 0) {
-            cp_async_wait_pending<1>();  // all but the next tile's inputs
-            if (by_map) glr_wait_boxes(bar + NS, k & 1);
+            if constexpr (by_map)
+                glr_wait_boxes(bar + NS, k & 1);
+            else
+                cp_async_wait_pending<1>();  // all but the next tile's inputs
             __syncwarp();
         }
         const int64_t ts = p.rows[kGlrOut].ts;
@@ -826,7 +832,7 @@ constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
 template <typename T, int EPI>
 constexpr int kGlrBwdWarpBytes = (EPI == 2 ? 6 : 4) * kGlrBwdStages<T> * kGlrBwdTok * kGlrSlab * (int)sizeof(T);
 
-template <typename T, bool VEC, int EPI, bool BACK>
+template <typename T, bool VEC, int EPI, int MODE>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
     glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI == 2 ? 6 : 4;
@@ -840,8 +846,8 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* const mine = reinterpret_cast<T*>(glr_smem + warp * kGlrBwdWarpBytes<T, EPI>);
 
-    const bool by_map = p.copy == kGlrByMap;
-    constexpr GlrOrder<TOK, BACK> at;
+    constexpr bool by_map = MODE != kGlrAsync;
+    constexpr GlrOrder<TOK, MODE> at;
     uint64_t* const bar = bars[warp];
 
     auto copy_inputs = [&](const GlrEntry& e, int stage) {
@@ -849,22 +855,24 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const int64_t ws = glr_first_step<true>(t, kGlrChunk) + warp * TOK;
         const int n = t.at < 0 ? 0 : glr_steps(t.len, ws, TOK);
         T* to = mine + stage * NT * ROWS;
-        if (by_map) {
+        if constexpr (by_map) {
             const int c = glr_channel(p, t);
             if constexpr (EPI == 2)
                 glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ, kGlrAdd>(to, maps, p, t, ws, n, c, bar + stage);
             else
                 glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout>(to, maps, p, t, ws, n, c, bar + stage);
-        } else if (n) {
-            const int left = p.D - glr_channel(p, t);
-            if constexpr (EPI == 2) {
-                glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ>(to, p, e, warp * TOK, n, left);
-                if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK, kGlrAdd>(to + 5 * ROWS, p, e, warp * TOK, n, left);
-            } else {
-                glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout>(to, p, e, warp * TOK, n, left);
+        } else {
+            if (n) {
+                const int left = p.D - glr_channel(p, t);
+                if constexpr (EPI == 2) {
+                    glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ>(to, p, e, warp * TOK, n, left);
+                    if (p.rows[kGlrAdd].p) glr_copy_rows<T, TOK, kGlrAdd>(to + 5 * ROWS, p, e, warp * TOK, n, left);
+                } else {
+                    glr_copy_rows<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout>(to, p, e, warp * TOK, n, left);
+                }
             }
+            cp_async_commit();
         }
-        cp_async_commit();
     };
     // the parameters' sums of the tile before, once a barrier has passed
     float* part = nullptr;
@@ -908,12 +916,14 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_z = in + 4 * ROWS, *in_add = in + 5 * ROWS;
         float2 nrg[TOK], nig[TOK], nu[TOK], hp[TOK];
         const float2 entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
-        cp_async_wait_pending<NS - 1>();
-        if (by_map) glr_wait_boxes(bar + stage, (k / NS) & 1);
+        if constexpr (by_map)
+            glr_wait_boxes(bar + stage, (k / NS) & 1);
+        else
+            cp_async_wait_pending<NS - 1>();
         __syncwarp();
         float2 P = glr_f2(1.f), q = glr_f2(0.f), h = glr_f2(0.f);
         if (n) {
-            if (n < TOK) glr_close_rows<T, TOK, NT, BACK>(in, at, n);
+            if (n < TOK) glr_close_rows<T, TOK, NT, MODE>(in, at, n);
             const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
             const float2 nr = glr_scaled<VEC>(p.r_bias, c0, nch, -kGlrLog2e);
             const float2 ni = glr_scaled<VEC>(p.i_bias, c0, nch, -kGlrLog2e);

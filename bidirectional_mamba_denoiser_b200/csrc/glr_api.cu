@@ -209,7 +209,8 @@ bool make_maps(bimamba::GlrMaps& maps, const GlrParams& k, int esz, int rows) {
 
 // Blocks that stay: what the SMs hold at 128 registers a thread.
 using TilesFn = void (*)(GlrParams, bimamba::GlrSync, bimamba::GlrMaps);
-int launch_tiles(TilesFn fn, TilesFn back, GlrParams& k, int esz, int64_t tiles, int tile_steps, int warps,
+// fns: by mode; without the maps' kernels where they cannot be used.
+int launch_tiles(const TilesFn (&fns)[3], GlrParams& k, int esz, int64_t tiles, int tile_steps, int warps,
                  size_t warp_bytes, unsigned flags, void* ws, cudaStream_t st) {
     const int64_t total = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
     // tickets run past the total by what the blocks take ahead
@@ -224,10 +225,10 @@ int launch_tiles(TilesFn fn, TilesFn back, GlrParams& k, int esz, int64_t tiles,
     const int64_t held = (int64_t)kSms * std::max(1, std::min(by_regs, by_smem));
     // maps take the host some microseconds: where every block has several tiles
     bimamba::GlrMaps maps = {};
-    if (back && k.copy == 16 && total >= 4 * held && make_maps(maps, k, esz, tile_steps / bimamba::kGlrWarps)) {
-        k.copy = bimamba::kGlrByMap;
-        if (k.reverse) fn = back;
-    }
+    int mode = bimamba::kGlrAsync;
+    if (fns[1] && k.copy == 16 && total >= 4 * held && make_maps(maps, k, esz, tile_steps / bimamba::kGlrWarps))
+        mode = k.reverse ? bimamba::kGlrMapReverse : bimamba::kGlrMapForward;
+    const TilesFn fn = fns[mode];
     if ((rc = ensure_smem(reinterpret_cast<const void*>(fn), bimamba::kGlrWarps * warp_bytes))) return rc;
     fn<<<(unsigned)std::min(total, held), warps * 32, smem, st>>>(k, y, maps);
     return launch_status();
@@ -238,17 +239,25 @@ int launch_fwd_epi(GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
     constexpr int TOK = bimamba::kGlrTok<T>, TILE = TOK * bimamba::kGlrWarps;
     const int64_t tiles = (k.L + TILE - 1) / TILE;
     const int warps = tiles > 1 ? bimamba::kGlrWarps : (int)((k.L + TOK - 1) / TOK);
-    TilesFn back = nullptr;  // (16-byte copies of the inputs come with paired outputs as good as always)
-    if constexpr (VEC) back = bimamba::glr_tile_fwd_kernel<T, VEC, EPI, true>;
-    return launch_tiles(bimamba::glr_tile_fwd_kernel<T, VEC, EPI, false>, back, k, (int)sizeof(T), tiles, TILE, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
+    using namespace bimamba;
+    TilesFn fns[3] = {glr_tile_fwd_kernel<T, VEC, EPI, kGlrAsync>, nullptr, nullptr};
+    if constexpr (VEC) {  // (inputs of whole 16 bytes hardly come with outputs of unpaired elements)
+        fns[1] = glr_tile_fwd_kernel<T, VEC, EPI, kGlrMapForward>;
+        fns[2] = glr_tile_fwd_kernel<T, VEC, EPI, kGlrMapReverse>;
+    }
+    return launch_tiles(fns, k, (int)sizeof(T), tiles, TILE, warps, bimamba::kGlrFwdWarpBytes<T, EPI>,
                         flags, ws, st);
 }
 
 template <typename T, bool VEC, int EPI>
 int launch_bwd_epi(GlrParams& k, unsigned flags, void* ws, cudaStream_t st) {
-    TilesFn back = nullptr;
-    if constexpr (VEC) back = bimamba::glr_tile_bwd_kernel<T, VEC, EPI, true>;
-    return launch_tiles(bimamba::glr_tile_bwd_kernel<T, VEC, EPI, false>, back, k, (int)sizeof(T), k.nchunk, bimamba::kGlrChunk, bimamba::kGlrWarps,
+    using namespace bimamba;
+    TilesFn fns[3] = {glr_tile_bwd_kernel<T, VEC, EPI, kGlrAsync>, nullptr, nullptr};
+    if constexpr (VEC) {  // (inputs of whole 16 bytes hardly come with outputs of unpaired elements)
+        fns[1] = glr_tile_bwd_kernel<T, VEC, EPI, kGlrMapForward>;
+        fns[2] = glr_tile_bwd_kernel<T, VEC, EPI, kGlrMapReverse>;
+    }
+    return launch_tiles(fns, k, (int)sizeof(T), k.nchunk, bimamba::kGlrChunk, bimamba::kGlrWarps,
                         bimamba::kGlrBwdWarpBytes<T, EPI>, flags, ws, st);
 }
 
