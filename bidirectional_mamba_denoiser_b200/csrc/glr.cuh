@@ -226,7 +226,9 @@ __device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
 // result is bit for bit that of the plain chain whatever the timing, while
 // only one hop in kGlrGroup waits on another tile's wait.  Each warp fetches one
 // of the eight pieces, asked for before its steps and looked at after them, so
-// what is there already costs no latency.  A published pair is one 64-bit word
+// what is there already costs no latency.  Where rows and slabs are so many
+// that a tile's predecessor is done long before its turn, a group is one tile:
+// only states are handed over.  A published pair is one 64-bit word
 // (or a float each), written once over an all-ones fill that no result has (a
 // NaN of that pattern is replaced), so it needs no flag and no fence.  Tiles
 // are taken in ticket order and a block works through its own in that order,
@@ -255,6 +257,7 @@ struct GlrSync {
     unsigned long long* map;     // [batch * slabs][tiles][64]: (P, h) of each channel
     float* state;                // [batch * slabs][groups][64]: state entering each group
     int64_t tiles, groups;
+    int shift;                   // a group is 1 << shift tiles: kGlrGroup, or one
     unsigned total;              // tiles of all rows and slabs
     int4* plan;                  // padded batches with a hand-over: [0] {count}, then the tiles that have steps in
                                  // ticket order, {at, row, length}; else null
@@ -317,8 +320,10 @@ __device__ __forceinline__ unsigned long long* glr_map(const GlrSync& y, const G
     return y.map + (t.rs * y.tiles + at) * kGlrSlab + 2 * (threadIdx.x & 31);
 }
 __device__ __forceinline__ float* glr_state(const GlrSync& y, const GlrTile& t, int at) {
-    return y.state + (t.rs * y.groups + at / kGlrGroup) * kGlrSlab + 2 * (threadIdx.x & 31);
+    return y.state + (t.rs * y.groups + (at >> y.shift)) * kGlrSlab + 2 * (threadIdx.x & 31);
 }
+// Tiles of t's group before it.
+__device__ __forceinline__ int glr_before(const GlrSync& y, const GlrTile& t) { return t.at & ((1 << y.shift) - 1); }
 __device__ __forceinline__ void glr_ask(GlrPiece& q, const GlrSync& y, const GlrTile& t, int warp) {
     if (warp == kGlrGroup - 1) {
         unsigned s0, s1;
@@ -327,10 +332,10 @@ __device__ __forceinline__ void glr_ask(GlrPiece& q, const GlrSync& y, const Glr
                      : "l"(glr_state(y, t, t.at))
                      : "memory");
         q.v[0] = s0, q.v[1] = s1;
-    } else if (warp < t.at % kGlrGroup) {
+    } else if (warp < glr_before(y, t)) {
         asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
                      : "=l"(q.v[0]), "=l"(q.v[1])
-                     : "l"(glr_map(y, t, t.at / kGlrGroup * kGlrGroup + warp))
+                     : "l"(glr_map(y, t, t.at - glr_before(y, t) + warp))
                      : "memory");
     } else {
         q.v[0] = q.v[1] = 0x3f800000ull;  // no such tile: P = 1, h = 0
@@ -767,7 +772,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                 P = glr_mul(P, make_float2(q.x, q.z));
                 h = glr_apply(q, h);
             }
-            if (publish) glr_publish_map(glr_map(y, t, t.at), P, h);
+            if (publish && y.shift) glr_publish_map(glr_map(y, t, t.at), P, h);
         }
         if (t.at) {
             got[warp][lane] = glr_wait_piece(y, piece, t, warp);
@@ -775,12 +780,12 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         const float4 from = got[kGlrGroup - 1][lane];
         float2 c = make_float2(from.y, from.w);
-        c = glr_through(got, c, t.at % kGlrGroup);
+        if (y.shift) c = glr_through(got, c, glr_before(y, t));
         if (warp == 0) {
             const float2 end = glr_fma(P, c, h);
             // the other tiles take a row's first state from here, not from h_in, which may be h_out
             if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
-            if (publish && (t.at + 1) % kGlrGroup == 0)
+            if (publish && ((t.at + 1) & ((1 << y.shift) - 1)) == 0)
                 glr_publish_state(glr_state(y, t, t.at + 1), end);
             if (last && p.h_out) glr_st2<VEC>(p.h_out + row, end, nch);
         }
@@ -969,7 +974,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         q = glr_fma(P, qw, q);
         P = glr_mul(P, Pw);
-        if (publish && warp == 0) glr_publish_map(glr_map(y, t, t.at), P, q);
+        if (publish && y.shift && warp == 0) glr_publish_map(glr_map(y, t, t.at), P, q);
         float4 mypiece = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t.at) {
             mypiece = glr_wait_piece(y, piece, t, warp);
@@ -996,12 +1001,12 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         __syncthreads();
         const float4 from = pieces[kGlrGroup - 1][lane];
         float2 c = make_float2(from.y, from.w);
-        c = glr_through(pieces, c, t.at % kGlrGroup);
+        if (y.shift) c = glr_through(pieces, c, glr_before(y, t));
         if (warp == 0) {
             const float2 end = glr_fma(P, c, q);
             // the other tiles take the last state's gradient from here, not from dh_out, which may be dh_in
             if (publish && t.at == 0) glr_publish_state(glr_state(y, t, 0), c);
-            if (publish && (t.at + 1) % kGlrGroup == 0)
+            if (publish && ((t.at + 1) & ((1 << y.shift) - 1)) == 0)
                 glr_publish_state(glr_state(y, t, t.at + 1), end);
             if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
         }

@@ -124,10 +124,13 @@ size_t handover_bytes(int batch, int D, int64_t tiles) {
 
 // Points y at the workspace and enqueues the all-ones fill (a row of one tile
 // hands nothing over and gets neither), and what a padded batch needs first.
-int make_sync(bimamba::GlrSync& y, const GlrParams& k, int64_t tiles, int tile_steps, unsigned flags, void* ws,
-              cudaStream_t st) {
+int make_sync(bimamba::GlrSync& y, const GlrParams& k, int64_t tiles, int tile_steps, bool grouped, unsigned flags,
+              void* ws, cudaStream_t st) {
     const int batch = k.batch, D = k.D;
-    const size_t bytes = tiles > 1 ? sync_bytes(batch, D, tiles) : 0;
+    const size_t chains = (size_t)batch * ((D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
+    const size_t maps = grouped ? chains * bimamba::kGlrSlab * (size_t)tiles * 8 : 0;
+    const size_t groups = grouped ? (size_t)(tiles + bimamba::kGlrGroup - 1) / bimamba::kGlrGroup : (size_t)tiles;
+    const size_t bytes = tiles > 1 ? 256 + maps + chains * bimamba::kGlrSlab * groups * 4 : 0;  // sync_bytes at most
     int4* plan = k.lengths && tiles > 1 ? reinterpret_cast<int4*>(static_cast<char*>(ws) + bytes) : nullptr;
     if (plan) {
         const int64_t blocks = std::max<int64_t>(k.batch * tiles, (int64_t)(bytes / 16384));
@@ -138,16 +141,16 @@ int make_sync(bimamba::GlrSync& y, const GlrParams& k, int64_t tiles, int tile_s
     }
     y = {};
     y.tiles = tiles;
-    y.groups = (tiles + bimamba::kGlrGroup - 1) / bimamba::kGlrGroup;
+    y.shift = grouped ? 3 : 0;
+    y.groups = (int64_t)groups;
     if (tiles <= 1) return BIMAMBA_OK;
-    const size_t chains = (size_t)batch * ((D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
     y.plan = plan;
     y.starve = (flags & BIMAMBA_TEST_STARVE) ? 1 : 0;
     y.wait_limit = y.starve ? kStarveWaitCycles : kWaitCycles;
     unsigned char* q = static_cast<unsigned char*>(ws);
     y.ticket = reinterpret_cast<unsigned int*>(q);
     y.map = reinterpret_cast<unsigned long long*>(q + 256);
-    y.state = reinterpret_cast<float*>(q + 256 + chains * bimamba::kGlrSlab * (size_t)tiles * 8);
+    y.state = reinterpret_cast<float*>(q + 256 + maps);
     if (plan) return BIMAMBA_OK;
     return cudaMemsetAsync(ws, 0xff, bytes, st) == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA;
 }
@@ -215,14 +218,17 @@ int launch_tiles(const TilesFn (&fns)[3], GlrParams& k, int esz, int64_t tiles, 
     const int64_t total = tiles * k.batch * ((k.D + bimamba::kGlrSlab - 1) / bimamba::kGlrSlab);
     // tickets run past the total by what the blocks take ahead
     if (total > 0x7fffffffLL) return BIMAMBA_ERR_UNSUPPORTED;
-    bimamba::GlrSync y;
-    int rc = make_sync(y, k, tiles, tile_steps, flags, ws, st);
-    if (rc) return rc;
-    y.total = (unsigned)total;
     const size_t smem = warps * warp_bytes;
     constexpr size_t kFixed = 17 * 1024 + 1024;  // static shared memory and the 1 KB that the system keeps
     const int by_regs = 16 / warps, by_smem = (int)(228 * 1024 / (smem + kFixed));
     const int64_t held = (int64_t)kSms * std::max(1, std::min(by_regs, by_smem));
+    // A tile's predecessor was taken as many tickets ago as there are rows times slabs: at half as many again as the
+    // blocks hold tiles it is done, and states alone are handed over (not in a padded batch, whose last tiles may be
+    // of one row).
+    bimamba::GlrSync y;
+    int rc = make_sync(y, k, tiles, tile_steps, k.lengths || 2 * (total / tiles) < 3 * held, flags, ws, st);
+    if (rc) return rc;
+    y.total = (unsigned)total;
     // maps take the host some microseconds: where every block has several tiles
     bimamba::GlrMaps maps = {};
     int mode = bimamba::kGlrAsync;
