@@ -598,10 +598,22 @@ def _vec(t, name: str, shape, device) -> int:
     """The address of a contiguous fp32 tensor of this shape (0 for None)."""
     if t is None:
         return 0
-    _check(t, name, shape, torch.float32, device)
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device:
+        _check(t, name, shape, torch.float32, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _like(t):
+    """An empty contiguous tensor of t's shape, dtype and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _several(n: int, shape, device):
+    """n empty fp32 tensors of one shape, from one allocation."""
+    return torch.empty((n, *shape), device=device, dtype=torch.float32).unbind(0) if n > 1 else \
+        [torch.empty(shape, device=device, dtype=torch.float32) for _ in range(n)]
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # (of a Stream object would take 2 us)
@@ -654,16 +666,22 @@ def _glr_inputs(x, r, i, params: dict, add, z, lengths):
     code = _dtype_code(dtype)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
+    at = _rows(x, "x")
     for t, name in ((r, "r"), (i, "i"), (add, "add"), (z, "z")):
-        _check(t, name, shape, dtype, dev)
+        if t is None:
+            at += _NO_ROWS
+            continue
+        if t.dtype != dtype or t.shape != shape or t.device != dev:
+            _check(t, name, shape, dtype, dev)
+        at += _rows(t, name)
+    n = 0
     if lengths is not None:
         _check(lengths, "lengths", (b,), torch.int32, dev)
-    inp = _GLR_INPUTS.pack(*_rows(x, "x"), *_rows(r, "r"), *_rows(i, "i"), *_rows(add, "add"), *_rows(z, "z"),
-                           _ptr(lengths) or 0, code)
+        n = _ptr(lengths)
     get, vec = params.get, (D,)
-    par = _GLR_PARAMS.pack(_vec(params["A"], "A", vec, dev), _vec(get("r_bias"), "r_bias", vec, dev),
-                           _vec(get("i_bias"), "i_bias", vec, dev))
-    return inp, par
+    return (_GLR_INPUTS.pack(*at, n, code),
+            _GLR_PARAMS.pack(_vec(params["A"], "A", vec, dev), _vec(get("r_bias"), "r_bias", vec, dev),
+                             _vec(get("i_bias"), "i_bias", vec, dev)))
 
 
 def bimamba_glr_fwd(x, r, i, params: dict, reverse: bool = False, add=None, z=None, lengths=None, h_in=None,
@@ -684,7 +702,7 @@ def bimamba_glr_fwd(x, r, i, params: dict, reverse: bool = False, add=None, z=No
     _check(out, "out", x.shape, x.dtype, dev)
     with _On(dev, stream) as on:
         if out is None:
-            out = torch.empty((b, L, D), device=dev, dtype=x.dtype)
+            out = _like(x)
         ws, ws_bytes = 0, 0
         if L > GLR_CHUNK or workspace is not None:  # a shorter call needs none
             workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D), dev)
@@ -713,17 +731,15 @@ def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = F
     for t, name in ((dx, "dx"), (dr, "dr"), (di, "di")):
         _check(t, name, x.shape, x.dtype, dev)
     with _On(dev, stream) as on:
-        def rows_like(t=None):
-            return t if t is not None else torch.empty(b, L, D, device=dev, dtype=x.dtype)
-
-        res = {"dx": rows_like(dx), "dr": rows_like(dr), "di": rows_like(di)}
+        res = {"dx": _like(x) if dx is None else dx, "dr": _like(x) if dr is None else dr,
+               "di": _like(x) if di is None else di}
         if add is not None:
-            res["dadd"] = rows_like()
+            res["dadd"] = _like(x)
         if z is not None:
-            res["dz"] = rows_like()
-        for name in ("A", "r_bias", "i_bias"):
-            if params.get(name) is not None:
-                res["d" + name] = torch.empty(D, device=dev, dtype=torch.float32)
+            res["dz"] = _like(x)
+        names = [k for k in ("A", "r_bias", "i_bias") if params.get(k) is not None]
+        for name, t in zip(names, _several(len(names), (D,), dev)):
+            res["d" + name] = t
         grads = [v for k in ("dx", "dr", "di", "dadd", "dz") for v in _rows(res.get(k), k)]
         sums = [res[k].data_ptr() if k in res else 0 for k in ("dA", "dr_bias", "di_bias")]
         workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D, True), dev)
@@ -779,9 +795,9 @@ def bimamba_block_norm_fwd(x, u=None, gate=None, post_w=None, gamma=None, beta=N
     with _On(dev, stream) as on:
         stored = x_out
         if stored is None and (u is not None or res_scale != 1.0):
-            stored = torch.empty((b, L, d), device=dev, dtype=x.dtype)
+            stored = _like(x)
         if y is None and norm:
-            y = torch.empty((b, L, d), device=dev, dtype=ty)
+            y = torch.empty((b, L, d), device=dev, dtype=ty) if u is None else _like(u)
         rc = lib.bimamba_block_norm_fwd(_ptr(x), _ptr(u), par, _ptr(stored), _ptr(y if norm else None),
                                         saved, _dtype_code(x.dtype), _dtype_code(ty), b, L, d, flags, on.handle)
     if rc != BIMAMBA_OK:
@@ -819,20 +835,22 @@ def bimamba_block_norm_bwd(dy, dx_out, x_out, stats, u=None, gate=None, post_w=N
     _check(stats, "stats", (b, L, 4), torch.float32, dev)
     _check(dx, "dx", x_out.shape, x_out.dtype, dev)
     with _On(dev, stream) as on:
-        def vec(like):
-            return torch.empty(like, device=dev, dtype=torch.float32)
-
-        res = {"dx": dx if dx is not None else torch.empty(b, L, d, device=dev, dtype=x_out.dtype)}
+        res = {"dx": _like(x_out) if dx is None else dx}
         if u is not None:
-            res["du"] = torch.empty(b, L, d, device=dev, dtype=ty)
+            res["du"] = _like(u)
+        # the vectors, those of one shape together
+        shapes = {}
         if gate is not None:
-            res["dgate"] = vec(gate.shape)
+            shapes["dgate"] = gate.shape
         if post_w is not None:
-            res["dpost_w"] = vec(post_w.shape)
+            shapes["dpost_w"] = post_w.shape
         if gamma is not None and dy is not None:
-            res["dgamma"] = vec(gamma.shape)
+            shapes["dgamma"] = gamma.shape
         if want_dbeta and dy is not None:
-            res["dbeta"] = vec((d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d))
+            shapes["dbeta"] = torch.Size((d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d))
+        for shape in set(shapes.values()):
+            names = [k for k, v in shapes.items() if v == shape]
+            res.update(zip(names, _several(len(names), shape, dev)))
         g = _NORM_GRADS.pack(*(_ptr(res.get(k)) or 0 for k in ("dx", "du", "dgate", "dpost_w", "dgamma", "dbeta")))
         workspace = _workspace_for(workspace, bimamba_block_norm_workspace_bytes(b, L, d), dev)
         rc = lib.bimamba_block_norm_bwd(_ptr(dy), _ptr(dx_out), _ptr(x_out), _ptr(u), _ptr(stats), par,
