@@ -39,9 +39,9 @@ struct GlrRows {
 };
 enum { kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ, kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors };
 
-// Maps of the inputs, kGlrR to kGlrZ: [batch][L][D], boxes of one warp's rows.
+// Maps of the inputs and the backward's outputs: [batch][L][D], boxes of one warp's rows.
 struct GlrMaps {
-    CUtensorMap m[kGlrZ + 1];
+    CUtensorMap m[kGlrTensors];
 };
 
 struct GlrParams {
@@ -597,6 +597,17 @@ __device__ __forceinline__ void glr_copy_boxes(T* to, const GlrMaps& maps, const
     };
     (one(TENSORS), ...);
 }
+// Rows of results, from shared memory by one lane; a whole warp's steps only.
+template <typename T>
+__device__ __forceinline__ void glr_store_box(const T* from, const CUtensorMap& map, int c, int t0, int b) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(&map)),
+                 "r"(smem_addr(from)), "r"(c), "r"(t0), "r"(b)
+                 : "memory");
+}
+// The lane's boxes are read (its shared memory may be written again).
+__device__ __forceinline__ void glr_boxes_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Bounded, like every wait.
 __device__ __forceinline__ void glr_wait_boxes(uint64_t* bar, unsigned parity) {
     if (mbar_try_wait(bar, parity)) return;
@@ -862,6 +873,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         T* to = mine + stage * NT * ROWS;
         if constexpr (by_map) {
             const int c = glr_channel(p, t);
+            if (lane == 0) glr_boxes_read();  // the stage's results
             if constexpr (EPI == 2)
                 glr_copy_boxes<T, TOK, kGlrR, kGlrI, kGlrX, kGlrDout, kGlrZ, kGlrAdd>(to, maps, p, t, ws, n, c, bar + stage);
             else
@@ -958,6 +970,8 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         agg[warp][lane] = make_float4(P.x, q.x, P.y, q.y);
         __syncthreads();
         t = e.t;  // (read again rather than kept)
+        // by maps a stage's results go out from it, so it is filled again half a tile later
+        if (by_map && NS == 2 && k > 0) copy_inputs(queue[(k + 1) % kGlrQueue], stage ^ 1);
         put_sums();
         part = p.part + chunk * 3 + c0;
         part_n = nch;
@@ -1018,10 +1032,17 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         for (int k = kGlrDx; k <= kGlrDz; ++k)
             to[k - kGlrDx] = p.rows[k].p + e.off[k] + (int64_t)p.rows[k].ts * (warp * TOK + TOK - 1) +
                              2 * lane * (int)sizeof(T);
-        auto put = [&](int tensor, int j, float2 v) {
-            glr_st2<VEC>(reinterpret_cast<T*>(to[tensor - kGlrDx] - (TOK - 1 - j) * (int64_t)p.rows[tensor].ts), v, nch);
+        // BOXES: into the row of the input that is read by now (dr for r, di for i, dx for x, dz for z, dadd for add)
+        auto put = [&](auto boxes, int tensor, int j, float2 v) {
+            if constexpr (decltype(boxes)::value) {
+                const int q = tensor == kGlrDr ? 0 : tensor == kGlrDi ? 1 : tensor == kGlrDx ? 2 : tensor == kGlrDz ? 4 : 5;
+                if (EPI == 1 && tensor == kGlrDadd) return;  // it is dout, as it lies there
+                glr_st2<true>(in + q * ROWS + at(j) + 2 * lane, v, 2);
+            } else {
+                glr_st2<VEC>(reinterpret_cast<T*>(to[tensor - kGlrDx] - (TOK - 1 - j) * (int64_t)p.rows[tensor].ts), v, nch);
+            }
         };
-        auto outputs = [&](auto full) {
+        auto outputs = [&](auto full, auto boxes) {
 #pragma unroll
             for (int j = TOK - 1; j >= 0; --j) {
                 if (!decltype(full)::value && j >= n) continue;
@@ -1036,10 +1057,10 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                     const float2 z = glr_row(in_z + at(j)), sz = glr_sigmoid2(z);
                     // silu'(z) = s (1 + z (1 - s))
                     const float2 ds = glr_fma(glr_mul(sz, z), make_float2(1.f - sz.x, 1.f - sz.y), sz);
-                    put(kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add + at(j)))), ds));
+                    put(boxes, kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add + at(j)))), ds));
                     dh = glr_mul(dh, glr_mul(z, sz));
                 }
-                if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(kGlrDadd, j, dh);
+                if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(boxes, kGlrDadd, j, dh);
                 const float2 G = glr_add(dh, q);
                 q = glr_fma(nu[j], G, G);
                 // a h_{s-1} - (a^2 / beta^2) w = h - w / beta^2 (both 0 with beta)
@@ -1047,27 +1068,46 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                 const float2 dla = glr_mul(G, make_float2(fmaf(-wb.x, rb.x, h.x), fmaf(-wb.y, rb.y, h.y)));
                 const float2 dr = glr_mul(glr_mul(nA, dla), glr_fma(nrg[j], nrg[j], nrg[j]));
                 const float2 Gw = glr_mul(G, w), di = glr_fma(Gw, nig[j], Gw);
-                put(kGlrDx, j, glr_mul(G, bi));
-                put(kGlrDr, j, dr);
-                put(kGlrDi, j, di);
+                put(boxes, kGlrDx, j, glr_mul(G, bi));
+                put(boxes, kGlrDr, j, dr);
+                put(boxes, kGlrDi, j, di);
                 sA = glr_fma(nrg[j], dla, sA);
                 sr = glr_add(sr, dr);
                 si = glr_add(si, di);
             }
         };
-        if (n == TOK)
-            outputs(std::true_type{});
-        else
-            outputs(std::false_type{});
+        if (n == TOK) {
+            outputs(std::true_type{}, std::bool_constant<by_map>{});
+            if constexpr (by_map) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    const int c = c0, first = (int)(glr_first_step<true>(t, kGlrChunk)) + warp * TOK;
+                    const int token = p.reverse ? t.len - first - TOK : first;
+                    glr_store_box(in, maps.m[kGlrDr], c, token, t.b);
+                    glr_store_box(in + ROWS, maps.m[kGlrDi], c, token, t.b);
+                    glr_store_box(in + 2 * ROWS, maps.m[kGlrDx], c, token, t.b);
+                    if (EPI == 2) glr_store_box(in + 4 * ROWS, maps.m[kGlrDz], c, token, t.b);
+                    if (EPI && p.rows[kGlrDadd].p)
+                        glr_store_box(in + (EPI == 1 ? 3 : 5) * ROWS, maps.m[kGlrDadd], c, token, t.b);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+        } else {
+            outputs(std::false_type{}, std::false_type{});
+        }
         sums[0][warp][lane] = make_float2(-sA.x, -sA.y);
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
         __syncwarp();  // every lane has read its rows
-        copy_inputs(queue[(k + NS) % kGlrQueue], stage);
+        if (!by_map || NS == 1) copy_inputs(queue[(k + NS) % kGlrQueue], stage);
     }
     __syncthreads();
     put_sums();
-    cp_async_wait_all();
+    if constexpr (by_map)
+        glr_boxes_read();
+    else
+        cp_async_wait_all();
     if (p.lengths) glr_pad<T>(p, y, reinterpret_cast<unsigned*>(queue));
 }
 

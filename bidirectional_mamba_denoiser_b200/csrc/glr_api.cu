@@ -182,8 +182,9 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Maps of the inputs that the call has; false where one cannot be mapped
-// (rows shared by tokens or by the batch).
+// Maps of the inputs that the call has, and of the backward's outputs; false
+// where one cannot be mapped (rows shared by tokens or by the batch, outputs
+// that start between 16 bytes).
 bool make_maps(bimamba::GlrMaps& maps, const GlrParams& k, int esz, int rows) {
     static const EncodeFn encode = [] {
         void* f = nullptr;
@@ -193,8 +194,9 @@ bool make_maps(bimamba::GlrMaps& maps, const GlrParams& k, int esz, int rows) {
             f = nullptr;
         return reinterpret_cast<EncodeFn>(f);
     }();
-    if (!encode) return false;
-    for (int q = bimamba::kGlrR; q <= bimamba::kGlrZ; ++q) {
+    const int last = k.part ? bimamba::kGlrDz : bimamba::kGlrZ;
+    if (!encode || (k.part && !starts_at(k, bimamba::kGlrDx, bimamba::kGlrDz, 16))) return false;
+    for (int q = bimamba::kGlrR; q <= last; ++q) {
         const GlrRows& r = k.rows[q];
         if (!r.p) continue;
         const int64_t ts = r.ts < 0 ? -(int64_t)r.ts : r.ts, bs = k.batch > 1 ? r.bs : ts * k.L;
