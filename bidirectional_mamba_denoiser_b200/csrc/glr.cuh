@@ -770,6 +770,9 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         if (t.at == 0 && warp == nwarp - 1) {
             const float2 c = glr_vec2<VEC>(p.h_in, row, nch);
             got[kGlrGroup - 1][lane] = make_float4(0.f, c.x, 0.f, c.y);
+        } else if (t.at && !y.shift && warp == kGlrGroup - 1) {
+            // no map to publish first: the state is waited for before the barrier, the only one then
+            got[kGlrGroup - 1][lane] = glr_wait_piece(y, piece, t, warp);
         }
         __syncthreads();
         t = e.t;  // (read again rather than kept)
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             }
             if (publish && y.shift) glr_publish_map(glr_map(y, t, t.at), P, h);
         }
-        if (t.at) {
+        if (t.at && y.shift) {
             got[warp][lane] = glr_wait_piece(y, piece, t, warp);
             __syncthreads();
         }
