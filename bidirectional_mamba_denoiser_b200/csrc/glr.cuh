@@ -37,7 +37,10 @@ struct GlrRows {
     int64_t bs;
     int ts;
 };
-enum { kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ, kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors };
+enum {
+    kGlrR, kGlrI, kGlrX, kGlrDout, kGlrAdd, kGlrZ,
+    kGlrOut, kGlrDx = kGlrOut, kGlrDr, kGlrDi, kGlrDadd, kGlrDz, kGlrTensors
+};
 
 // Maps of the inputs and the backward's outputs: [batch][L][D], boxes of one warp's rows.
 struct GlrMaps {
@@ -79,10 +82,15 @@ __device__ __forceinline__ float glr_rsqrt(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
 }
-// The larger of two, NaN if either is.
+// The larger and the smaller of two, NaN if either is.
 __device__ __forceinline__ float glr_max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float glr_min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -242,6 +250,22 @@ __device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
 // copy by tensor maps, one box a tensor that one lane asks for (in reverse the
 // box's rows are the steps backwards); others by cp.async, whose addresses cost
 // the warp some 20 instructions a tensor.
+//
+// What bounds it and what the choices measured (b 8, L 2048, D 4096 bf16; its
+// 537 MB take 82 us at 6.56 TB/s):
+//   one thread a channel, step after step                    1339 us
+//   a block a tile, loads to registers                        360
+//   blocks that stay, rows copied ahead                        234
+//   pieces asked for early, offsets a tile once, full tiles
+//   without selects                                            151
+//   copies by maps                                             137
+//   states alone handed over, one barrier                      131
+// Special functions take 59 us, the copies alone 109 us with the gates left
+// out; issue slots are 60 % used by 16 warps of 128 registers, 48 of some 81
+// instructions a pair and step being the gates'.  Shorter warps' runs would
+// spread a tile's fixed instructions (some 300 a warp) over fewer steps, longer
+// ones do not fit the registers.  Scalar constants in place of packed ones: the
+// same time.
 constexpr int kGlrSlab = 64;
 constexpr int kGlrGroup = 8;
 static_assert(kGlrGroup == 8, "a piece for each warp");
@@ -252,8 +276,8 @@ static __device__ unsigned int g_glr_error;
 constexpr int kGlrPad = 16, kGlrGone = 32;  // other sectors
 
 struct GlrSync {
-    unsigned int* ticket;        // [0] the tickets, [kGlrPad] those of glr_pad, [kGlrGone] zero once a wait ran out; all ones before the
-                                 // launch.  Null: one tile a row, nothing to hand over
+    unsigned int* ticket;        // [0] the tickets, [kGlrPad] those of glr_pad, [kGlrGone] zero once a wait ran
+                                 // out; all ones before the launch.  Null: one tile a row, nothing to hand over
     unsigned long long* map;     // [batch * slabs][tiles][64]: (P, h) of each channel
     float* state;                // [batch * slabs][groups][64]: state entering each group
     int64_t tiles, groups;
@@ -449,11 +473,14 @@ __global__ void __launch_bounds__(256)
         if (plan && (there || item == 0)) {
             if (threadIdx.x == 0) before = count = 0;
             __syncthreads();
+            int stand = 0, all = 0;
             for (int j = threadIdx.x; j < p.batch; j += blockDim.x) {
                 const int own = (int)((glr_len(p, j) + tile_steps - 1) / tile_steps);
-                atomicAdd(&before, min(own, here) + (j < b && own > here));
-                atomicAdd(&count, own);
+                stand += min(own, here) + (j < b && own > here);
+                all += own;
             }
+            atomicAdd(&before, stand);
+            atomicAdd(&count, all);
             __syncthreads();
             if (threadIdx.x == 0) {
                 if (there) plan[1 + before] = make_int4(here, (int)b, (int)len, 0);
@@ -648,7 +675,7 @@ __device__ __forceinline__ void glr_close_rows(T* rows, GlrOrder<TOK, MODE> at, 
 }
 // -bias log2 e and A log2 e of a pair, kept finite so that a closed gate wins.
 __device__ __forceinline__ float2 glr_finite(float2 v) {
-    return make_float2(glr_max_nan(v.x, -3.4e38f), glr_max_nan(v.y, -3.4e38f));
+    return make_float2(glr_min_nan(glr_max_nan(v.x, -3.4e38f), 3.4e38f), glr_min_nan(glr_max_nan(v.y, -3.4e38f), 3.4e38f));
 }
 template <bool VEC>
 __device__ __forceinline__ float2 glr_scaled(const float* v, int c, int nch, float by) {
@@ -673,7 +700,8 @@ constexpr int kGlrFwdWarpBytes = (3 * kGlrFwdStages<EPI> + EPI) * kGlrTok<T> * k
 
 template <typename T, bool VEC, int EPI, int MODE>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
-    glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
+    glr_tile_fwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y,
+                        const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrTok<T>, NS = kGlrFwdStages<EPI>, ROWS = TOK * kGlrSlab;
     extern __shared__ __align__(128) unsigned char glr_smem[];
     __shared__ float4 aggs[2][kGlrWarps][32];      // (P, h) of each warp
@@ -844,7 +872,12 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 // end to its left.  A warp's steps share one product P for both scans, the
 // recomputed states (ascending, from the saved state that enters the tile)
 // and q (descending).  The second half reads x, dout, add and z again from
-// shared memory, so a warp's next copies start after it.
+// shared memory, and by maps it leaves its results in the rows that it has
+// read, from where a lane sends them as boxes; so a stage is filled again once
+// they are out.  b 8, L 2048, D 4096 bf16: 283 us of 143 us for its 940 MB; issue
+// slots 62 % used, some 180 instructions a pair and step (68 the second half's, 30
+// the gates', 40 a tile's fixed ones over 8 steps); the registers hold no more
+// steps.  (One thread a channel: 2956 us with the forward; a block a tile: 465.)
 constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
 template <typename T>
 constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
@@ -853,7 +886,8 @@ constexpr int kGlrBwdWarpBytes = (EPI == 2 ? 6 : 4) * kGlrBwdStages<T> * kGlrBwd
 
 template <typename T, bool VEC, int EPI, int MODE>
 __global__ void __launch_bounds__(kGlrWarps * 32, 2)
-    glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y, const __grid_constant__ GlrMaps maps) {
+    glr_tile_bwd_kernel(const __grid_constant__ GlrParams p, const __grid_constant__ GlrSync y,
+                        const __grid_constant__ GlrMaps maps) {
     constexpr int TOK = kGlrBwdTok, NS = kGlrBwdStages<T>, ROWS = TOK * kGlrSlab, NT = EPI == 2 ? 6 : 4;
     extern __shared__ __align__(128) unsigned char glr_smem[];
     __shared__ float4 agg[kGlrWarps][32];   // (P, q) of each warp

@@ -435,8 +435,9 @@ int bimamba_out_proj(const void *y, const void *w_out, int batch, int64_t L, int
  * layer's z.  A call with few tokens, h_in and h_out is the serving form (one new
  * token, or an active block of them).
  *   Padded batches: row b has len = lengths[b] tokens (clamped to [0, L]; L
- * without lengths).  Tokens at and after len are not read, their outputs
- * (and gradients) are written as 0, and a row of no tokens has h_out = h_in. */
+ * without lengths).  Tokens at and after len have no influence, whatever they
+ * hold; their outputs (and gradients) are written as 0, and a row of no tokens has
+ * h_out = h_in. */
 
 /* Scan the row from its last token to its first. */
 #define BIMAMBA_GLR_REVERSE 0x8u

@@ -127,3 +127,12 @@ def test_a_wait_that_runs_out_is_reported(bm, backward):
     fwd = T.forward(bm, g)
     T.check_forward(fwd, ref)
     T.check_backward(T.backward(bm, g, fwd[2]), ref)
+
+
+def test_infinite_parameters(bm):
+    """A = -inf forgets at every step, r_bias = inf opens and i_bias = -inf closes a gate, in padded rows too."""
+    c = T.case(3, 150, 16, "fp32", seed=10, state=True, lengths=[150, 0, 77])
+    c["params"]["A"][3] = -float("inf")
+    c["params"]["r_bias"][5] = float("inf")
+    c["params"]["i_bias"][7] = -float("inf")
+    T.check_forward(T.forward(bm, T.to_gpu(c)), T.oracle_of(c))
