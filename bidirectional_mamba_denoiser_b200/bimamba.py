@@ -610,12 +610,6 @@ def _like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _several(n: int, shape, device):
-    """n empty fp32 tensors of one shape, from one allocation."""
-    return torch.empty((n, *shape), device=device, dtype=torch.float32).unbind(0) if n > 1 else \
-        [torch.empty(shape, device=device, dtype=torch.float32) for _ in range(n)]
-
-
 _raw_stream = torch._C._cuda_getCurrentRawStream  # (of a Stream object would take 2 us)
 
 
@@ -737,9 +731,9 @@ def bimamba_glr_bwd(dout, x, r, i, params: dict, chunk_states, reverse: bool = F
             res["dadd"] = _like(x)
         if z is not None:
             res["dz"] = _like(x)
-        names = [k for k in ("A", "r_bias", "i_bias") if params.get(k) is not None]
-        for name, t in zip(names, _several(len(names), (D,), dev)):
-            res["d" + name] = t
+        for name in ("A", "r_bias", "i_bias"):
+            if params.get(name) is not None:
+                res["d" + name] = torch.empty_like(params[name])
         grads = [v for k in ("dx", "dr", "di", "dadd", "dz") for v in _rows(res.get(k), k)]
         sums = [res[k].data_ptr() if k in res else 0 for k in ("dA", "dr_bias", "di_bias")]
         workspace = _workspace_for(workspace, bimamba_glr_workspace_bytes(b, L, D, True), dev)
@@ -805,6 +799,7 @@ def bimamba_block_norm_fwd(x, u=None, gate=None, post_w=None, gamma=None, beta=N
     return (x if stored is None else stored), (y if norm else None)
 
 
+@functools.lru_cache(maxsize=256)
 def bimamba_block_norm_workspace_bytes(batch: int, L: int, d: int) -> int:
     return int(lib.bimamba_block_norm_workspace_bytes(batch, L, d))
 
@@ -838,20 +833,18 @@ def bimamba_block_norm_bwd(dy, dx_out, x_out, stats, u=None, gate=None, post_w=N
         res = {"dx": _like(x_out) if dx is None else dx}
         if u is not None:
             res["du"] = _like(u)
-        # the vectors, those of one shape together
-        shapes = {}
         if gate is not None:
-            shapes["dgate"] = gate.shape
+            res["dgate"] = torch.empty_like(gate)
         if post_w is not None:
-            shapes["dpost_w"] = post_w.shape
+            res["dpost_w"] = torch.empty_like(post_w)
         if gamma is not None and dy is not None:
-            shapes["dgamma"] = gamma.shape
+            res["dgamma"] = torch.empty_like(gamma)
         if want_dbeta and dy is not None:
-            shapes["dbeta"] = torch.Size((d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d))
-        for shape in set(shapes.values()):
-            names = [k for k, v in shapes.items() if v == shape]
-            res.update(zip(names, _several(len(names), shape, dev)))
-        g = _NORM_GRADS.pack(*(_ptr(res.get(k)) or 0 for k in ("dx", "du", "dgate", "dpost_w", "dgamma", "dbeta")))
+            res["dbeta"] = torch.empty_like(gamma) if gamma is not None else torch.empty(
+                (d,) if flags & BIMAMBA_NORM_GAMMA_SHARED else (b, d), device=dev, dtype=torch.float32)
+        get = res.get
+        g = _NORM_GRADS.pack(_ptr(res["dx"]), *[0 if t is None else t.data_ptr() for t in (
+            get("du"), get("dgate"), get("dpost_w"), get("dgamma"), get("dbeta"))])
         workspace = _workspace_for(workspace, bimamba_block_norm_workspace_bytes(b, L, d), dev)
         rc = lib.bimamba_block_norm_bwd(_ptr(dy), _ptr(dx_out), _ptr(x_out), _ptr(u), _ptr(stats), par,
                                         g, _dtype_code(x_out.dtype), _dtype_code(ty), b, L, d, flags,
