@@ -905,23 +905,25 @@ __device__ __forceinline__ void bn_set(float* p, const float* v) {
         *p = v[0];
 }
 
-// A lane's E elements of a row, or of an fp32 vector (`other` without it, 0 past d).
+// A lane's E elements of a row that starts for it at `from`, or of an fp32
+// vector (`other` without it, 0 past d).  It has `mine` accesses, `step`
+// elements apart; the elements of the others are 0.
 template <int E, int P, typename T>
-__device__ __forceinline__ void bn_gather(const T* row, float (&v)[E], int g, int G, int d) {
+__device__ __forceinline__ void bn_gather(const T* from, float (&v)[E], int step, int mine) {
 #pragma unroll
     for (int j = 0; j < E / P; ++j) {
-        const int c = (g + G * j) * P;
 #pragma unroll
         for (int e = 0; e < P; ++e) v[j * P + e] = 0.f;
-        if (c < d) bn_get<P>(row + c, v + j * P);
+        if (j < mine) bn_get<P>(from, v + j * P);
+        from += step;
     }
 }
 template <int E, int P, typename T>
-__device__ __forceinline__ void bn_scatter(T* row, const float (&v)[E], int g, int G, int d) {
+__device__ __forceinline__ void bn_scatter(T* to, const float (&v)[E], int step, int mine) {
 #pragma unroll
     for (int j = 0; j < E / P; ++j) {
-        const int c = (g + G * j) * P;
-        if (c < d) bn_set<P>(row + c, v + j * P);
+        if (j < mine) bn_set<P>(to, v + j * P);
+        to += step;
     }
 }
 template <int E, int P>
@@ -944,7 +946,7 @@ __device__ __forceinline__ float2 bn_group_sum2(float2 v, int G, BnShared& sh, i
     return v;
 }
 template <int E, int P>
-__device__ __forceinline__ float2 bn_group_stats(const float (&v)[E], const BlockNormParams& p, int g, int G,
+__device__ __forceinline__ float2 bn_group_stats(const float (&v)[E], const BlockNormParams& p, int mine, int G,
                                                  BnShared& sh, int& turn) {
     const float per = 1.f / (float)p.d;
     float mu = 0.f, q = 0.f;
@@ -957,7 +959,7 @@ __device__ __forceinline__ float2 bn_group_stats(const float (&v)[E], const Bloc
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float c = v[e] - mu;
-        if ((g + G * (e / P)) * P < p.d) q = fmaf(c, c, q);
+        if (e / P < mine) q = fmaf(c, c, q);
     }
     return make_float2(mu, rsqrtf(bn_group_sum2(make_float2(q, 0.f), G, sh, turn).x * per + p.eps));
 }
@@ -973,6 +975,7 @@ __global__ void __launch_bounds__(256, 2) block_norm_fwd_pack_kernel(const Block
     __shared__ BnShared sh;
     int turn = 0;
     const int d = p.d, g = threadIdx.x % G, group = threadIdx.x / G, groups = blockDim.x / G;
+    const int step = G * P, accesses = d > g * P ? (d - g * P + step - 1) / step : 0;
     const int64_t b = blockIdx.y, tiles = (p.L + R - 1) / R;
     const int xs = bn_pack_bytes(R, d, sizeof(TS)), us = bn_pack_bytes(R, d, sizeof(TU));
     const int64_t all = p.batch * p.L * d;
@@ -1007,29 +1010,31 @@ __global__ void __launch_bounds__(256, 2) block_norm_fwd_pack_kernel(const Block
         // whole warps (or the block) go round together: a group without a row has one of no columns
         for (int r0 = 0; r0 < n; r0 += groups) {
             const bool own = r0 + group < n;
-            const int r = own ? r0 + group : n - 1, w = own ? d : 0;
+            const int r = own ? r0 + group : n - 1, mine = own ? accesses : 0;
+            TS* const xr = xt + r * d + g * P;
+            TU* const ur = ut + r * d + g * P;
             float x[E], u[E];
             float2 sx = make_float2(0.f, 1.f), su = make_float2(0.f, 1.f);
-            bn_gather<E, P>(xt + r * d, x, g, G, w);
+            bn_gather<E, P>(xr, x, step, mine);
             if (p.u) {
-                bn_gather<E, P>(ut + r * d, u, g, G, w);
+                bn_gather<E, P>(ur, u, step, mine);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; ++e) u[e] = 0.f;
             }
             if constexpr (POST) {
-                su = bn_group_stats<E, P>(u, p, g, G, sh, turn);
+                su = bn_group_stats<E, P>(u, p, accesses, G, sh, turn);
 #pragma unroll
                 for (int e = 0; e < E; ++e) u[e] = (u[e] - su.x) * su.y * post_w[e];
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = bn_round<TS>(fmaf(gate[e], u[e], p.res_scale * x[e]));
-            if (own && p.x_out) bn_scatter<E, P>(xt + r * d, x, g, G, d);
+            if (p.x_out) bn_scatter<E, P>(xr, x, step, mine);
             if (p.y) {
-                sx = bn_group_stats<E, P>(x, p, g, G, sh, turn);
+                sx = bn_group_stats<E, P>(x, p, accesses, G, sh, turn);
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = fmaf(gamma[e], (x[e] - sx.x) * sx.y, beta[e]);
-                if (own) bn_scatter<E, P>(ut + r * d, x, g, G, d);
+                bn_scatter<E, P>(ur, x, step, mine);
             }
             if (own && p.stats && g == 0) {
                 float* st = p.stats + (b * p.L + tile * R + r) * 4;
@@ -1050,6 +1055,7 @@ __global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const Block
     __shared__ BnShared sh;
     int turn = 0;
     const int d = p.d, g = threadIdx.x % G, group = threadIdx.x / G, groups = blockDim.x / G;
+    const int step = G * P, accesses = d > g * P ? (d - g * P + step - 1) / step : 0;
     const int64_t b = blockIdx.y, tiles = (p.L + R - 1) / R;
     const int xs = bn_pack_bytes(R, d, sizeof(TS)), us = bn_pack_bytes(R, d, sizeof(TU));
     const int64_t all = p.batch * p.L * d;
@@ -1092,22 +1098,22 @@ __global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const Block
         fetch(tile + gridDim.x, s ^ 1);
         for (int r0 = 0; r0 < n; r0 += groups) {
             const bool own = r0 + group < n;
-            const int r = own ? r0 + group : n - 1, width = own ? d : 0;
+            const int r = own ? r0 + group : n - 1, mine = own ? accesses : 0, at = r * d + g * P;
             const float* st = p.stats + (b * p.L + tile * R + r) * 4;
             const float mu = st[0], rs = st[1], mu_u = st[2], rs_u = st[3];
             float D[E], u[E];
             if (p.dx_out) {
-                bn_gather<E, P>(dxt + r * d, D, g, G, width);
+                bn_gather<E, P>(dxt + at, D, step, mine);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; ++e) D[e] = 0.f;
             }
-            if (p.u) bn_gather<E, P>(ut + r * d, u, g, G, width);
+            if (p.u) bn_gather<E, P>(ut + at, u, step, mine);
             if (p.dy) {
                 float v[E], dy[E];
                 float2 sum = make_float2(0.f, 0.f);
-                bn_gather<E, P>(xt + r * d, v, g, G, width);
-                bn_gather<E, P>(dyt + r * d, dy, g, G, width);  // 0 past d, and so is what follows from it
+                bn_gather<E, P>(xt + at, v, step, mine);
+                bn_gather<E, P>(dyt + at, dy, step, mine);  // 0 past d, and so is what follows from it
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     v[e] = (v[e] - mu) * rs;
@@ -1125,7 +1131,7 @@ __global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const Block
             float o[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = p.res_scale * D[e];
-            if (own) bn_scatter<E, P>(xt + r * d, o, g, G, d);
+            bn_scatter<E, P>(xt + at, o, step, mine);
             if (!p.u) continue;
             if constexpr (POST) {
                 float2 t = make_float2(0.f, 0.f);
@@ -1152,7 +1158,7 @@ __global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const Block
                     o[e] = gate[e] * D[e];
                 }
             }
-            if (own) bn_scatter<E, P>(ut + r * d, o, g, G, d);
+            bn_scatter<E, P>(ut + at, o, step, mine);
         }
         __syncthreads();
         bn_store_run<TS>(stage, p.dx, rx);
@@ -1163,10 +1169,10 @@ __global__ void __launch_bounds__(512, 1) block_norm_bwd_pack_kernel(const Block
     // the groups' column sums, in order
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(bn_smem);  // [groups][4][d]
-    bn_scatter<E, P>(sums + (group * 4 + 0) * d, sg, g, G, d);
-    bn_scatter<E, P>(sums + (group * 4 + 1) * d, sw, g, G, d);
-    bn_scatter<E, P>(sums + (group * 4 + 2) * d, sm, g, G, d);
-    bn_scatter<E, P>(sums + (group * 4 + 3) * d, sb, g, G, d);
+    bn_scatter<E, P>(sums + (group * 4 + 0) * d + g * P, sg, step, accesses);
+    bn_scatter<E, P>(sums + (group * 4 + 1) * d + g * P, sw, step, accesses);
+    bn_scatter<E, P>(sums + (group * 4 + 2) * d + g * P, sm, step, accesses);
+    bn_scatter<E, P>(sums + (group * 4 + 3) * d + g * P, sb, step, accesses);
     __syncthreads();
     float* q = p.part + ((int64_t)b * p.nseg + blockIdx.x) * 4 * d;
     for (int c = threadIdx.x; c < 4 * d; c += blockDim.x) {

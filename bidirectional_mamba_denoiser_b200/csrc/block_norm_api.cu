@@ -182,7 +182,7 @@ int launch_pack(BlockNormParams& k, cudaStream_t st) {
 
 // Which form.  The copying one where a row fills a warp and is whole groups of
 // eight; the packed one for other rows up to kPackMaxD columns (65,536 rows of 129
-// bf16: forward 60 us, backward 64, the plain form 111 and 638; of 56: 17 and 25,
+// bf16: forward 44 us, backward 61, the plain form 111 and 638; of 56: 17 and 26,
 // plain 31 and 49); the plain one for wider odd rows, for pointers that no 16-byte
 // access can use, and for batch rows of a few tokens that have vectors of their
 // own (a block a batch row would be idle).
