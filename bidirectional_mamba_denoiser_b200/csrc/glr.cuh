@@ -261,7 +261,7 @@ __device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
 //   copies by maps                                             137
 //   states alone handed over, one barrier                      131
 // Special functions take 59 us, the copies alone 109 us with the gates left
-// out; issue slots are 60 % used by 16 warps of 128 registers, 48 of some 81
+// out; issue slots are 60 % used by 16 warps of 128 registers, some 30 of 81
 // instructions a pair and step being the gates'.  Shorter warps' runs would
 // spread a tile's fixed instructions (some 300 a warp) over fewer steps, longer
 // ones do not fit the registers.  Scalar constants in place of packed ones: the
