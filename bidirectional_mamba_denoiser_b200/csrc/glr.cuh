@@ -15,7 +15,10 @@
 // The backward recomputes the gates and the states from the inputs and the
 // state that the forward saved every kGlrChunk steps (fp32, 4 / 64 bytes an
 // element) instead of reading a stored h: that is less traffic than bf16
-// states would be, and exact.
+// states would be, and rounds none of them to bf16.  A decay may be anything
+// down to 0, and what it multiplies is as small, so a comes with its own
+// relative accuracy and dla from the terms above, which both have a factor a
+// (as h - w / beta^2 they would cancel to it, and leave the rounding of h).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -173,10 +176,12 @@ __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(gl
 // with |f| <= 1/2 (n by adding and subtracting 1.5 2^23), 2^f - 1 = f p(f) with
 // p of degree 5 (minimax of the relative error by Remez exchange, 1.1e-8), and
 // 2^l - 1 = (2^n - 1) + 2^n (2^f - 1), where 2^n - 1 is exact or far from
-// cancelling.  Below l = -126 the power is as good as 0.
-__device__ __forceinline__ float2 glr_ex2m1(float2 l) {
+// cancelling.  `pow` is 2^l itself = 2^n + 2^n (2^f - 1): of 2^l - 1 it could
+// not be had, whose rounding is all that is left of a small power.  Below l =
+// -126.5 it is 0 (n = -127, whose 2^n has no bits).
+__device__ __forceinline__ float2 glr_ex2m1(float2 l, float2& pow) {
     constexpr float kMagic = 12582912.f;
-    l = make_float2(glr_max_nan(l.x, -126.f), glr_max_nan(l.y, -126.f));
+    l = make_float2(glr_max_nan(l.x, -127.f), glr_max_nan(l.y, -127.f));
     const float2 m = glr_add(l, kMagic);
     const float2 f = glr_sub(l, glr_add(m, -kMagic));
     float2 q = glr_fma(f, glr_f2(0.00015403512225020677f), 0.0013390735257416964f);
@@ -188,6 +193,7 @@ __device__ __forceinline__ float2 glr_ex2m1(float2 l) {
     // 2^n, its exponent from the low bits of m
     const float2 s = make_float2(__uint_as_float((__float_as_uint(m.x) << 23) + 0x3f800000u),
                                  __uint_as_float((__float_as_uint(m.y) << 23) + 0x3f800000u));
+    pow = glr_fma(q, s, s);
     return glr_fma(q, s, glr_add(s, -1.f));
 }
 
@@ -195,7 +201,7 @@ __device__ __forceinline__ float2 glr_ex2m1(float2 l) {
 // need no operand of ones, which costs two registers or two moves each time.
 // r, i: raw activations; nr, ni: -bias log2 e; nA2: -A log2 e.
 struct GlrGate2 {
-    float2 nrg, nu, a, nb2, di;  // -rg, a - 1, a, -beta^2 = a^2 - 1, 1 / ig
+    float2 nrg, a, nb2, di;  // -rg, a, -beta^2 = a^2 - 1, 1 / ig
 };
 __device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, float2 ni, float2 nA2) {
     GlrGate2 g;
@@ -203,19 +209,30 @@ __device__ __forceinline__ GlrGate2 glr_gate2(float2 r, float2 i, float2 nr, flo
     const float2 dr = glr_add(make_float2(glr_ex2(er.x), glr_ex2(er.y)), 1.f);
     g.di = glr_add(make_float2(glr_ex2(ei.x), glr_ex2(ei.y)), 1.f);
     g.nrg = make_float2(glr_rcp(-dr.x), glr_rcp(-dr.y));
-    g.nu = glr_ex2m1(glr_mul(nA2, g.nrg));
-    g.a = glr_add(g.nu, 1.f);
-    g.nb2 = glr_fma(g.nu, g.a, g.nu);
+    const float2 nu = glr_ex2m1(glr_mul(nA2, g.nrg), g.a);  // a - 1
+    g.nb2 = glr_fma(nu, g.a, nu);
     return g;
 }
 // The smallest normal, added under every 1 / beta: 0 / 0 becomes 0, and down to
 // beta^2 = 1e-31 nothing else changes.
 constexpr float kGlrTiny = 1.17549435e-38f;
+// a once more, from what the backward keeps of a gate.
+__device__ __forceinline__ float2 glr_decay(float2 nA2, float2 nrg) {
+    const float2 l = glr_mul(nA2, nrg);
+    return make_float2(glr_ex2(l.x), glr_ex2(l.y));
+}
 // -beta ig with one special function: b2 / sqrt(b2 di^2) = sqrt(b2) / di (where
 // di^2 overflows, an input gate below e^-44, it counts as closed).
 __device__ __forceinline__ float2 glr_minus_beta_ig(float2 nb2, float2 di) {
     const float2 v = glr_mul(glr_mul(make_float2(kGlrTiny - nb2.x, kGlrTiny - nb2.y), di), di);
     return glr_mul(nb2, make_float2(glr_rsqrt(v.x), glr_rsqrt(v.y)));
+}
+// -beta alone, and 1 / beta of it (0 times it stays 0).
+__device__ __forceinline__ float2 glr_minus_beta(float2 nb2) {
+    return glr_mul(nb2, make_float2(glr_rsqrt(kGlrTiny - nb2.x), glr_rsqrt(kGlrTiny - nb2.y)));
+}
+__device__ __forceinline__ float2 glr_over_beta(float2 nb) {
+    return make_float2(glr_rcp(1e-24f - nb.x), glr_rcp(1e-24f - nb.y));
 }
 
 // ---------------------------------------------------------------- tiles in scan order
@@ -869,15 +886,18 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 // Backward, tiles of kGlrChunk steps: they are walked from the last step to
 // the first (tile `at` from the end of the row's own tiles), and what they
 // hand over is q = a G, which the affine map of a tile takes from its right
-// end to its left.  A warp's steps share one product P for both scans, the
-// recomputed states (ascending, from the saved state that enters the tile)
-// and q (descending).  The second half reads x, dout, add and z again from
+// end to its left.  A warp's steps share one running product P for both scans,
+// the recomputed states (from the saved state that enters the tile) and q,
+// which at the warp's first step is sum_s P_s dh_s.  Of each step the registers
+// keep rg, ig, beta and the state before it; a is one more ex2 where it is wanted
+// again (a small a cannot be had from beta, nor a small beta from a, and there
+// is no room for both).  The second half reads x, dout, add and z again from
 // shared memory, and by maps it leaves its results in the rows that it has
 // read, from where a lane sends them as boxes; so a stage is filled again once
-// they are out.  b 8, L 2048, D 4096 bf16: 283 us of 143 us for its 940 MB; issue
-// slots 62 % used, some 180 instructions a pair and step (68 the second half's, 30
-// the gates', 40 a tile's fixed ones over 8 steps); the registers hold no more
-// steps.  (One thread a channel: 2956 us with the forward; a block a tile: 465.)
+// they are out.  b 8, L 2048, D 4096 bf16: 285 us of 143 us for its 940 MB; issue
+// slots 61 % used, special functions 42 %, some 180 instructions a pair and step
+// (68 the second half's, 30 the gates', 40 a tile's fixed ones over 8 steps); the
+// registers hold no more steps.  (One thread a channel: 2956 us with the forward; a block a tile: 465.)
 constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
 template <typename T>
 constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
@@ -961,14 +981,14 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         const int stage = NS == 2 ? k & 1 : 0;
         const int c0 = glr_channel(p, t) + 2 * lane;
         const int nch = p.D - c0 > 1 ? 2 : (p.D - c0 > 0 ? 1 : 0);
-        const int64_t s0 = glr_first_step<true>(t, kGlrChunk), s1 = s0 + kGlrChunk, row = (int64_t)t.b * p.D + c0;
+        const int64_t s0 = glr_first_step<true>(t, kGlrChunk), row = (int64_t)t.b * p.D + c0;
         const int64_t chunk = ((int64_t)t.b * p.nchunk + s0 / kGlrChunk) * p.D;
         const int n = glr_steps(t.len, s0 + warp * TOK, TOK);
         GlrPiece piece;
         if (t.at) glr_ask(piece, y, t, warp);
         T* in = mine + stage * NT * ROWS;
         const T *in_x = in + 2 * ROWS, *in_d = in + 3 * ROWS, *in_z = in + 4 * ROWS, *in_add = in + 5 * ROWS;
-        float2 nrg[TOK], nig[TOK], nu[TOK], hp[TOK];
+        float2 nrg[TOK], nig[TOK], nb[TOK], hp[TOK];  // -rg, -ig, -beta, a state
         const float2 entering = glr_vec2<VEC>(p.chunk, chunk + c0, nch);
         if constexpr (by_map)
             glr_wait_boxes(bar + stage, (k / NS) & 1);
@@ -984,23 +1004,19 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 const GlrGate2 g = glr_gate2(glr_row(in + at(j)), glr_row(in + ROWS + at(j)), nr, ni, nA2);
-                const float2 w = glr_mul(glr_minus_beta_ig(g.nb2, g.di), glr_minus_row(in_x + at(j)));
                 nrg[j] = g.nrg;
                 nig[j] = make_float2(glr_rcp(-g.di.x), glr_rcp(-g.di.y));
-                nu[j] = g.nu;
+                nb[j] = glr_minus_beta(g.nb2);
+                const float2 w = glr_mul(glr_mul(nb[j], nig[j]), glr_row(in_x + at(j)));
                 hp[j] = h;  // the state before step j, from a zero state at the warp's first
                 P = glr_mul(P, g.a);
                 h = glr_fma(g.a, h, w);
-            }
-#pragma unroll
-            for (int j = TOK - 1; j >= 0; --j) {
                 float2 dh = glr_row(in_d + at(j));
                 if constexpr (EPI == 2) {
                     const float2 z = glr_row(in_z + at(j));
                     dh = glr_mul(dh, glr_mul(z, glr_sigmoid2(z)));
                 }
-                const float2 G = glr_add(q, dh);
-                q = glr_fma(nu[j], G, G);  // a G
+                q = glr_fma(P, dh, q);  // what the step's dh is at the warp's first
             }
         }
         aggh[warp][lane] = h;
@@ -1035,6 +1051,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
         }
         pieces[warp][lane] = mypiece;
         // the states before the warp's steps, from the one that enters the tile
+        const float2 nA2 = glr_scaled<VEC>(p.A, c0, nch, -kGlrLog2e);
         if (n) {
             float2 c = entering;
 #pragma unroll
@@ -1046,7 +1063,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 hp[j] = glr_add(c, hp[j]);
-                c = glr_fma(nu[j], c, c);
+                c = glr_mul(glr_decay(nA2, nrg[j]), c);
             }
         }
         __syncthreads();
@@ -1083,26 +1100,23 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 #pragma unroll
             for (int j = TOK - 1; j >= 0; --j) {
                 if (!decltype(full)::value && j >= n) continue;
-                const float2 nb2 = glr_fma(nu[j], nu[j], glr_add(nu[j], nu[j]));
-                // 1 / beta
-                const float2 rb = make_float2(glr_rsqrt(kGlrTiny - nb2.x), glr_rsqrt(kGlrTiny - nb2.y));
-                const float2 bi = glr_mul(glr_mul(nb2, rb), nig[j]);  // beta ig
-                const float2 w = glr_mul(bi, glr_row(in_x + at(j)));
-                const float2 h = glr_add(glr_fma(nu[j], hp[j], hp[j]), w);
+                const float2 a = glr_decay(nA2, nrg[j]);
+                const float2 bi = glr_mul(nb[j], nig[j]), w = glr_mul(bi, glr_row(in_x + at(j)));
+                const float2 ah = glr_mul(a, hp[j]);
                 float2 dh = glr_row(in_d + at(j));
                 if constexpr (EPI == 2) {
                     const float2 z = glr_row(in_z + at(j)), sz = glr_sigmoid2(z);
                     // silu'(z) = s (1 + z (1 - s))
                     const float2 ds = glr_fma(glr_mul(sz, z), make_float2(1.f - sz.x, 1.f - sz.y), sz);
-                    put(boxes, kGlrDz, j, glr_mul(glr_mul(dh, glr_add(h, glr_row(in_add + at(j)))), ds));
+                    put(boxes, kGlrDz, j, glr_mul(glr_mul(dh, glr_add(glr_add(ah, w), glr_row(in_add + at(j)))), ds));
                     dh = glr_mul(dh, glr_mul(z, sz));
                 }
                 if (EPI == 1 || (EPI == 2 && p.rows[kGlrDadd].p)) put(boxes, kGlrDadd, j, dh);
                 const float2 G = glr_add(dh, q);
-                q = glr_fma(nu[j], G, G);
-                // a h_{s-1} - (a^2 / beta^2) w = h - w / beta^2 (both 0 with beta)
-                const float2 wb = glr_mul(w, rb);
-                const float2 dla = glr_mul(G, make_float2(fmaf(-wb.x, rb.x, h.x), fmaf(-wb.y, rb.y, h.y)));
+                q = glr_mul(a, G);
+                // a h_{s-1} - (a / beta)^2 w
+                const float2 ab = glr_mul(a, glr_over_beta(nb[j])), wab = glr_mul(w, ab);
+                const float2 dla = glr_mul(G, make_float2(fmaf(-wab.x, ab.x, ah.x), fmaf(-wab.y, ab.y, ah.y)));
                 const float2 dr = glr_mul(glr_mul(nA, dla), glr_fma(nrg[j], nrg[j], nrg[j]));
                 const float2 Gw = glr_mul(G, w), di = glr_fma(Gw, nig[j], Gw);
                 put(boxes, kGlrDx, j, glr_mul(G, bi));
