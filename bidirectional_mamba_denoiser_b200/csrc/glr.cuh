@@ -690,7 +690,7 @@ __device__ __forceinline__ void glr_close_rows(T* rows, GlrOrder<TOK, MODE> at, 
         }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a box may overwrite them
 }
-// -bias log2 e and A log2 e of a pair, kept finite so that a closed gate wins.
+// -bias log2 e, -A log2 e or -A of a pair, kept finite so that a closed gate wins.
 __device__ __forceinline__ float2 glr_finite(float2 v) {
     return make_float2(glr_min_nan(glr_max_nan(v.x, -3.4e38f), 3.4e38f), glr_min_nan(glr_max_nan(v.y, -3.4e38f), 3.4e38f));
 }
@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
             if (last && p.dh_in) glr_st2<VEC>(p.dh_in + row, end, nch);
         }
         q = glr_fma(Pw, c, qw);
-        const float2 nA = glr_mul(glr_vec2<VEC>(p.A, c0, nch), glr_f2(-1.f));
+        const float2 nA = glr_scaled<VEC>(p.A, c0, nch, -1.f);  // finite: where A is infinite a factor beside it is 0
         // where the warp's steps go, from its last to its first
         char* to[kGlrDz - kGlrDx + 1];
 #pragma unroll
@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
                 // a h_{s-1} - (a / beta)^2 w
                 const float2 ab = glr_mul(a, glr_over_beta(nb[j])), wab = glr_mul(w, ab);
                 const float2 dla = glr_mul(G, make_float2(fmaf(-wab.x, ab.x, ah.x), fmaf(-wab.y, ab.y, ah.y)));
-                const float2 dr = glr_mul(glr_mul(nA, dla), glr_fma(nrg[j], nrg[j], nrg[j]));
+                const float2 dr = glr_mul(glr_mul(nA, glr_fma(nrg[j], nrg[j], nrg[j])), dla);
                 const float2 Gw = glr_mul(G, w), di = glr_fma(Gw, nig[j], Gw);
                 put(boxes, kGlrDx, j, glr_mul(G, bi));
                 put(boxes, kGlrDr, j, dr);

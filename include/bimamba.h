@@ -458,7 +458,8 @@ typedef struct {
 
 /* Parameters of the direction, fp32 device pointers. */
 typedef struct {
-    const float *A;       /* [d_inner], <= 0: the log decay of a wide-open gate (a positive entry is undefined) */
+    const float *A;       /* [d_inner], <= 0: the log decay of a wide-open gate (a positive entry is undefined;
+                             with -inf an open gate forgets everything, and dA, dr and dr_bias are 0) */
     const float *r_bias;  /* [d_inner] or NULL (= 0) */
     const float *i_bias;  /* [d_inner] or NULL (= 0) */
 } bimamba_glr_params_t;

@@ -149,3 +149,24 @@ def test_a_state_that_only_decays(bm, A, L, reverse):
     _relative(res["dx"], ref["dx"], bound + 16 * e, "dx")
     rg = 1 / (1 + np.exp(-c["r"].double().numpy() - c["params"]["r_bias"].double().numpy()))
     _relative(res["dr"], ref["dr"], bound + 8 * e + e * (1 + 6 * (1 - rg)) / (1 - rg), "dr")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_with_infinite_parameters(bm, dtype, gated):
+    """A = -inf forgets at every step: A e^(A rg) goes to 0, and with it the channel's dr and dA; a gate that is closed
+    there keeps the state.  r_bias = inf opens and i_bias = -inf closes a gate.  In a padded batch, whose closed steps are no
+    part of it.  (In fp64 -1e30 is as good as -inf, and leaves 0 times it 0.)"""
+    c = T.case(3, 150, 16, dtype, seed=4, gated=gated, state=True, lengths=[150, 0, 77])
+    c["params"]["A"][3] = c["params"]["A"][9] = -float("inf")
+    c["params"]["r_bias"][5], c["params"]["i_bias"][7] = float("inf"), -float("inf")
+    c["r"][:, 20:30, 9] = -float("inf")
+    g = T.to_gpu(c)
+    c["params"]["A"][3] = c["params"]["A"][9] = -1e30
+    ref = T.oracle_of(c, False, True)
+    fwd = T.forward(bm, g)
+    T.check_forward(fwd, ref)
+    res = T.backward(bm, g, fwd[2])
+    T.check_backward(res, ref)
+    for k in ("dr", "dA", "dr_bias"):
+        assert bool((res[k][..., [3, 9]] == 0).all()), k
