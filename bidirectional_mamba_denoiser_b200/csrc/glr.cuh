@@ -174,11 +174,12 @@ __device__ __forceinline__ float2 glr_sigmoid2(float2 v) { return make_float2(gl
 // 2^l - 1 for l <= 0, to fp32's relative accuracy however small |l| is, on the
 // FP32 pipe (the special-function unit is the forward's scarcest): l = n + f
 // with |f| <= 1/2 (n by adding and subtracting 1.5 2^23), 2^f - 1 = f p(f) with
-// p of degree 5 (minimax of the relative error by Remez exchange, 1.1e-8), and
-// 2^l - 1 = (2^n - 1) + 2^n (2^f - 1), where 2^n - 1 is exact or far from
-// cancelling.  `pow` is 2^l itself = 2^n + 2^n (2^f - 1): of 2^l - 1 it could
-// not be had, whose rounding is all that is left of a small power.  Below l =
-// -126.5 it is 0 (n = -127, whose 2^n has no bits).
+// p of degree 5 (minimax of the relative error by Remez exchange, with its
+// coefficients as fp32 holds them within 2.2e-8), and 2^l - 1 = (2^n - 1) + 2^n
+// (2^f - 1), where 2^n - 1 is exact or far from cancelling.  `pow` is 2^l itself
+// = 2^n + 2^n (2^f - 1): of 2^l - 1 it could not be had, whose rounding is all
+// that is left of a small power.  Below l = -126.5 it is 0 (n = -127, whose 2^n
+// has no bits).
 __device__ __forceinline__ float2 glr_ex2m1(float2 l, float2& pow) {
     constexpr float kMagic = 12582912.f;
     l = make_float2(glr_max_nan(l.x, -127.f), glr_max_nan(l.y, -127.f));
@@ -897,7 +898,8 @@ __global__ void __launch_bounds__(kGlrWarps * 32, 2)
 // they are out.  b 8, L 2048, D 4096 bf16: 285 us of 143 us for its 940 MB; issue
 // slots 61 % used, special functions 42 %, some 180 instructions a pair and step
 // (68 the second half's, 30 the gates', 40 a tile's fixed ones over 8 steps); the
-// registers hold no more steps.  (One thread a channel: 2956 us with the forward; a block a tile: 465.)
+// registers hold no more steps.  (One thread a channel: 2956 us with the forward;
+// a block a tile: 465.)
 constexpr int kGlrBwdTok = kGlrChunk / kGlrWarps;
 template <typename T>
 constexpr int kGlrBwdStages = sizeof(T) == 2 ? 2 : 1;
