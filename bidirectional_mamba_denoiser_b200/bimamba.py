@@ -183,7 +183,9 @@ lib = _load()
 
 
 def bimamba_device_error(reset: bool = True) -> int:
-    """The device error word (0 = no kernel gave up waiting); synchronises."""
+    """The device error word (0 = no kernel gave up waiting; 1: for a tile load,
+    2: a Mamba-2 reverse block for its forward, 4: a tile of the gated linear
+    recurrence for an earlier one); synchronises."""
     return int(lib.bimamba_device_error(1 if reset else 0))
 
 

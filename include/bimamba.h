@@ -597,11 +597,15 @@ int bimamba_features(const bimamba_inputs_t *in, const bimamba_params_t *p, int 
                      float *u, float *delta, void *cuda_stream);
 
 /* Read (and, if reset != 0, clear) the error word of the current device.
- * Kernels never wait without bound: a wait for a tile that gives up after
- * about two seconds sets bit 0 (a tile load that never arrived), a Mamba-2
- * reverse CTA's wait for its forward that gives up sets bit 1, and the kernel
- * finishes with undefined output instead of hanging.  Synchronises the
- * device.  Returns the word, or BIMAMBA_ERR_CUDA if it cannot be read. */
+ * Kernels never wait without bound: a wait that gives up after about two
+ * seconds sets a bit, and the kernel finishes with undefined output instead of
+ * hanging.
+ *   bit 0  a tile load that never arrived (the gated linear recurrence's too)
+ *   bit 1  a Mamba-2 reverse CTA that waited for its forward
+ *   bit 2  a tile of bimamba_glr_fwd or bimamba_glr_bwd that waited for what an
+ *          earlier tile of its row hands over
+ * Synchronises the device.  Returns the word, or BIMAMBA_ERR_CUDA if it cannot
+ * be read. */
 int bimamba_device_error(int reset);
 
 /* Human-readable text for a status code (static storage). */
