@@ -552,6 +552,8 @@ const char* bimamba_status_string(int status) {
 
 int bimamba_device_error(int reset) {
     unsigned int word = 0, glr = 0;
+    // the copies wait for the legacy stream only, not for work on a non-blocking one
+    if (cudaDeviceSynchronize() != cudaSuccess) return BIMAMBA_ERR_CUDA;
     if (cudaMemcpyFromSymbol(&word, bimamba::g_device_error, sizeof(word)) != cudaSuccess) return BIMAMBA_ERR_CUDA;
     if (reset) {
         const unsigned int zero = 0;
