@@ -22,7 +22,7 @@
 // walks a run of one batch row's tokens, every thread copying its own columns
 // of the rows ahead into shared memory (cp.async; a thread reads back only what
 // it copied, so no barrier), with the vectors in registers for the whole run.
-// Odd and narrow rows: tiles of neighbouring rows as flat runs of bytes.  What
+// Odd and narrow rows, and those whose copies ahead do not fit: tiles of neighbouring rows as flat runs of bytes.  What
 // neither takes: a warp or a block a row, straight from memory.
 //
 // 16,384 rows of 2048 bf16 (268 MB, 41 us at 6.56 TB/s): forward 71 us straight
@@ -30,7 +30,8 @@
 // packed arithmetic, 50 with two column groups a thread.  Backward (403 MB, 61
 // us): 168, 105, 83 with packed arithmetic and the statistics asked for a row ahead,
 // 80 with fp32 rows in whole sectors (which took 65,536 rows of 1920 with an fp32
-// stream from 313 to 250 us of 230).  What is left is the chain of a row's sums.
+// stream from 313 us to 249-280, from run to run, of 230).  What is left is the
+// chain of a row's sums.
 #pragma once
 
 #include <cuda_bf16.h>

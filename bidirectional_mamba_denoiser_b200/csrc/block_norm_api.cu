@@ -101,7 +101,8 @@ constexpr size_t kMaxRunSmem = 200 * 1024;
 int run_threads(int d, int k) { return ((d / 8 + k - 1) / k + 31) / 32 * 32; }
 
 // The copying form: 32 to 512 threads of K = 1 or 2 groups of eight columns.
-// False where the copies ahead would not fit (wide fp32 rows in the backward).
+// False where the copies ahead would not fit: the backward of fp32 rows of 3080 to
+// 4096 columns with an fp32 branch (above, K = 2 has fewer stages).
 template <bool BWD, typename TS, typename TU, int K>
 bool launch_run_k(BlockNormParams& k, cudaStream_t st, int& rc) {
     constexpr int pieces = BWD ? bimamba::kBnBwdPieces<TS, TU, K> : bimamba::kBnFwdPieces<TS, TU, K>;
@@ -181,7 +182,8 @@ int launch_pack(BlockNormParams& k, cudaStream_t st) {
 }
 
 // Which form.  The copying one where a row fills a warp and is whole groups of
-// eight; the packed one for other rows up to kPackMaxD columns (65,536 rows of 129
+// eight, if its copies ahead fit; the packed one for other rows up to kPackMaxD
+// columns (8192 fp32 rows of 4096 in the backward: 220 us of 123; 65,536 rows of 129
 // bf16: forward 44 us, backward 61, the plain form 111 and 638; of 56: 17 and 26,
 // plain 31 and 49); the plain one for wider odd rows, for pointers that no 16-byte
 // access can use, and for batch rows of a few tokens that have vectors of their
@@ -206,8 +208,9 @@ int launch(BlockNormParams& k, bool vec, bool chunks, bimamba_dtype_t ts, bimamb
 }
 
 // Row segments of the backward per batch row, each with its own column sums:
-// one for each block that the SMs hold (128 registers a thread), but at least
-// 8 rows a segment.
+// one for each block that the SMs hold at 128 registers a thread, but at least
+// 8 rows a segment.  (In fp32 shared memory holds fewer, and the rest follow:
+// 16,384 rows of 2048 take 148 us of 123.)
 int segments(int batch, int64_t L, int d) {
     const int threads = d % 8 == 0 && d >= 256 ? std::min(512, (d / 8 + 31) / 32 * 32) : std::max(256, pack_lanes(d, true));
     const int held = std::max(1, std::min(16, 512 / threads));
